@@ -9,6 +9,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+# translation units of libdreamer.so
+UNITS = ("dreamer.cu", "route_noalloc.cu", "kv4.cu")
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-shared", "-Xptxas", "-v"] if os.environ.get("DREAMER_PTXAS_VERBOSE") else \
         ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -30,11 +32,11 @@ def _sources(exts=(".cu", ".cuh", ".h")):
 
 def build(force: bool = False, verbose: bool = False) -> list:
     outs = []
+    units = [os.path.join(CSRC, u) for u in UNITS]
     lib = os.path.join(HERE, "libdreamer.so")
     deps = [p for p in _sources() if not p.endswith("inputs_gen.cu")]
     if force or not _newer(lib, deps):
-        cmd = ["nvcc", *ARCH, *FLAGS, "-o", lib, os.path.join(CSRC, "dreamer.cu"),
-               os.path.join(CSRC, "route_noalloc.cu")]
+        cmd = ["nvcc", *ARCH, *FLAGS, "-t", "0", "-o", lib, *units]
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
@@ -42,8 +44,7 @@ def build(force: bool = False, verbose: bool = False) -> list:
     hooks = os.path.join(HERE, "libdreamer_testhooks.so")
     if force or not _newer(hooks, deps):
         cmd = ["nvcc", *ARCH, *FLAGS, "-DDREAMER_TEST_HOOKS",
-               "-DDREAMER_WAIT_LIMIT_NS=20000000ull", "-o", hooks,
-               os.path.join(CSRC, "dreamer.cu"), os.path.join(CSRC, "route_noalloc.cu")]
+               "-DDREAMER_WAIT_LIMIT_NS=20000000ull", "-t", "0", "-o", hooks, *units]
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)

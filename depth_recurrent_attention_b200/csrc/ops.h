@@ -1,0 +1,56 @@
+// Launchers of the handle-free attention operators, shared by their C entry points and by the
+// handle's paths (dreamer.cu).  Arguments are checked by the callers; a launcher returns a
+// DREAMER_* code for what only it can see (a tensor map, a CUDA error).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace dreamer {
+namespace ops {
+
+// Launch options of a handle's path: programmatic dependent launch (the previous operation on
+// the stream is a kernel that the launched one waits for itself).
+struct LaunchOpt {
+  bool pdl = false;
+};
+
+// ---- 4-bit cache: one depth of one handle, or a caller's cache --------------------------
+constexpr int KV4_BLOCK = 64;  // tokens of a block
+constexpr int KV4_GROUP = 64;  // channels that share a (scale, offset) pair
+
+struct Kv4Cache {
+  uint8_t *data;  // [B][Hkv][cap / 64][ng * 4608]
+  int B, Hkv, d, cap;
+};
+// bytes of one block: K codes, V codes [ng][64][32], K pairs, V pairs [ng][64][2] bf16
+constexpr int kv4_block_bytes(int d) { return (d / KV4_GROUP) * KV4_BLOCK * 2 * (32 + 4); }
+
+struct Kv4Rows {
+  const void *k, *v;  // store: source rows; load: destination rows (not const there)
+  long ldk, ldv;      // row strides in elements; head j at column j * d
+  const int *cu;      // [B + 1] rows of sequence b: cu[b] .. cu[b + 1] - 1; null: row b is sequence b's
+  const int *start;   // [B] position of a sequence's first row
+  int n_rows;
+  int dtype;          // 0 float32, 1 bfloat16
+  int zero_rest;      // load: rows of no sequence become zeros
+  int *err;           // device error flag or null
+};
+int kv4_store(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o = LaunchOpt());
+int kv4_load(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o = LaunchOpt());
+
+struct Kv4Attn {
+  const void *q;
+  long ldq;        // row stride of q in elements
+  void *out;
+  long ldo;
+  const int *lens;  // [B]
+  int len_add;      // keys of sequence b: lens[b] + len_add
+  int Hq;
+  int dtype;
+  float scale;
+  int *err;
+};
+int kv4_attn(const Kv4Cache &c, const Kv4Attn &a, cudaStream_t s, LaunchOpt o = LaunchOpt());
+
+}  // namespace ops
+}  // namespace dreamer

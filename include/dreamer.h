@@ -217,6 +217,58 @@ int dreamer_bias_update_counts(dreamer_handle *h, float lambda, const int32_t *c
 int dreamer_route_balance(dreamer_handle *h, int depth, float *lorenz, float *gini,
                           dreamer_stream stream);
 
+/* ---- A 4-bit cache of attention keys and values ---------------------------------------------
+ * These entry points need no handle and allocate nothing.  A group is 64 consecutive channels
+ * of one head of one token: s = (max - min) / 15 and m = min, both rounded to bfloat16,
+ * c = round((x - m) / s) in 0..15 (half to even; 0 where s = 0); the value held is s c + m.
+ * A group with a NaN, an infinity or a magnitude above 2^126 is held, and read back, as NaN.
+ *
+ * `data` holds one depth: [batch][n_kv_heads][capacity / 64] blocks of 64 tokens, a block being
+ * K codes [head_dim / 64][64][32 bytes] (channel 2i in the low half of byte i), V codes
+ * likewise, K pairs (s, m) [head_dim / 64][64][2] bfloat16, V pairs likewise:
+ * dreamer_kv4_bytes() bytes in all, 0.5625 a value.
+ *
+ * Conventions: device pointers, 16-byte aligned; rows at a stride (ld*, in elements, a multiple
+ * of 16 bytes) with head j at columns j * head_dim ..; dtype 0 = float32, 1 = bfloat16.
+ * head_dim is 64 or 128 and capacity a multiple of 64 (DREAMER_ERR_UNSUPPORTED otherwise).
+ * `status` is NULL or a device int32 that the caller clears: a device-side error (a position or
+ * a length outside the cache, an expired bounded wait) sets it to a non-zero value; such rows
+ * are skipped, such a sequence attends to nothing.  Calls are asynchronous on `stream`, use the
+ * current device and may run at once on several streams (on different rows, where they write). */
+typedef struct {
+  void *data;
+  int batch, n_kv_heads, head_dim, capacity;
+} dreamer_kv4_cache;
+
+/* Bytes of one depth's cache, or 0 for sizes that it does not take.                         */
+int64_t dreamer_kv4_bytes(int batch, int n_kv_heads, int head_dim, int capacity);
+
+/* Quantise rows into the cache: rows cu_rows[b] .. cu_rows[b+1]-1 of k and v (n_rows rows of
+ * n_kv_heads * head_dim) become positions start[b], start[b] + 1, ... of sequence b.
+ * cu_rows [batch+1] int32, not decreasing; start [batch] int32.  Rows before cu_rows[0] and
+ * from cu_rows[batch] on belong to no sequence and are not stored; nor is a position outside
+ * 0 .. capacity-1 (reported).                                                               */
+int dreamer_kv4_store(const dreamer_kv4_cache *cache, const void *k, int64_t ldk, const void *v,
+                      int64_t ldv, const int32_t *cu_rows, const int32_t *start, int n_rows,
+                      int dtype, int32_t *status, dreamer_stream stream);
+
+/* The same rows read back: s c + m rounded to dtype.  Rows of no sequence, or of a position
+ * outside the cache, are left as they were (zero_rest = 0) or become zeros (zero_rest = 1).  */
+int dreamer_kv4_load(const dreamer_kv4_cache *cache, void *k, int64_t ldk, void *v, int64_t ldv,
+                     const int32_t *cu_rows, const int32_t *start, int n_rows, int dtype,
+                     int zero_rest, int32_t *status, dreamer_stream stream);
+
+/* Attention of one query token a sequence over the cache, grouped heads: query head j of
+ * sequence b attends positions 0 .. lens[b]-1 of key head j / (n_heads / n_kv_heads),
+ *   out = sum_i softmax_i(scale q . k_i) v_i,
+ * and a sequence with lens[b] = 0 gets zeros.  q, out: [batch] rows of n_heads * head_dim of
+ * dtype (out may be q); lens [batch] int32; n_heads a multiple of n_kv_heads.  Sums, softmax
+ * and products are float32, the weights of the output product bfloat16 for bfloat16 (float32
+ * in three terms for float32).  What lies in the cache behind lens[b] is not used.          */
+int dreamer_attn_kv4(const dreamer_kv4_cache *cache, const void *q, int64_t ldq, void *out,
+                     int64_t ldo, const int32_t *lens, int n_heads, int dtype, float scale,
+                     int32_t *status, dreamer_stream stream);
+
 /* Instrumentation.  Stages of the depth step, in launch order: */
 enum {
   DREAMER_STAGE_NORM = 0,     /* RMSNorm of the residual stream                          */
