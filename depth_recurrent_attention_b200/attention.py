@@ -1,4 +1,4 @@
-"""Attention operators without a handle: a 4-bit cache of keys and values (quantised as it is
+"""Attention operators without a handle: causal attention over packed prompts, and a 4-bit cache of keys and values (quantised as it is
 written, read back, attended by single tokens).
 
 Every operator runs in libdreamer's CUDA kernels (include/dreamer.h); this module checks
@@ -39,7 +39,8 @@ def _lib():
         L.dreamer_kv4_store.argtypes = rows
         L.dreamer_kv4_load.argtypes = rows[:9] + [i, vp, vp]
         L.dreamer_attn_kv4.argtypes = [vp, vp, i64, vp, i64, vp, i, i, f, vp, vp]
-        for n in ("dreamer_kv4_store", "dreamer_kv4_load", "dreamer_attn_kv4"):
+        L.dreamer_attn_packed.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i, i, i, i, i, i, f, vp, vp]
+        for n in ("dreamer_kv4_store", "dreamer_kv4_load", "dreamer_attn_kv4", "dreamer_attn_packed"):
             getattr(L, n).restype = i
         _fns = L
     return _fns
@@ -97,6 +98,41 @@ def _call(fn, what, device, stream, *args):
         with torch.cuda.device(device):
             _check(fn(*args, stream.cuda_stream), what)
     return stream
+
+
+def attn_packed(q, k, v, cu_seqlens, out=None, scale=None, status=None, stream=None):
+    """Causal attention over packed prompts of different lengths, with grouped heads.
+
+    q [tokens][n_heads][dim], k and v [tokens][n_kv_heads][dim]; cu_seqlens int32 [prompts + 1],
+    not decreasing: prompt i holds rows cu_seqlens[i] .. cu_seqlens[i+1]-1.  Query head j uses key
+    head j // (n_heads // n_kv_heads); scale (positive) defaults to 1 / sqrt(dim).  Returns
+    `out`, [tokens][n_heads][dim]; rows of no prompt are not written.  bfloat16 takes dim 64 and
+    128, float32 also 16 and 32.  Boundaries out of order or outside the rows set `status`."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q: a CUDA tensor")
+    dev = q.device
+    ldq = _rows("q", q, dev)
+    n, hq, d = q.shape
+    ldk = _rows("k", k, dev, None, d, q.dtype, n)
+    hk = k.shape[1]
+    ldv = _rows("v", v, dev, hk, d, q.dtype, n)
+    if hk < 1 or hq < 1 or hq % hk:
+        raise ValueError(f"{hq} query heads over {hk} key heads")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens: int32 [prompts + 1]")
+    cu = _ints("cu_seqlens", cu_seqlens, dev, cu_seqlens.shape[0])
+    if out is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            out = torch.empty((n, hq, d), dtype=q.dtype, device=dev)
+    ldo = _rows("out", out, dev, hq, d, q.dtype, n)
+    scale = _scale(scale, d)
+    if not scale > 0:
+        raise ValueError("scale: positive")
+    if n:
+        _call(_lib().dreamer_attn_packed, "dreamer_attn_packed", dev, stream, q.data_ptr(), ldq,
+              k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, cu, cu_seqlens.shape[0] - 1,
+              n, hq, hk, d, _DTYPES[q.dtype], scale, _status(status, dev))
+    return out
 
 
 class KV4Cache:

@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # translation units of libdreamer.so
-UNITS = ("dreamer.cu", "route_noalloc.cu", "kv4.cu")
+UNITS = ("dreamer.cu", "route_noalloc.cu", "attn_packed.cu", "kv4.cu")
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-shared", "-Xptxas", "-v"] if os.environ.get("DREAMER_PTXAS_VERBOSE") else \
         ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",

@@ -1,0 +1,768 @@
+// Causal attention over packed prompts of different lengths, with grouped heads.
+//
+// Rows of all prompts lie one behind the other; cu[i] .. cu[i + 1] - 1 are prompt i's.  Token t
+// of a prompt attends the prompt's tokens up to itself:
+//   out[t, h] = sum_{j <= t} softmax_j(scale q[t, h] . k[j, h / G]) v[j, h / G].
+//
+// Work items are (row tile of a prompt, head).  The host knows the number of rows and prompts
+// only, so it launches the most items that they can make, and a block finds its own from cu:
+// items are ordered by their tile index, the highest (most keys) first over all prompts, so
+// that long items start first and a block's item costs one search over the tile indices with
+// the prompts spread over a warp's lanes.
+//
+// What a row must not see does not touch it, whatever it holds: masked scores are replaced, not
+// added to; value rows behind the prompt's end are cleared in shared memory; and where a value
+// of the diagonal block is not finite (0 x infinity would reach the rows before it), the block's
+// output product is done row by row on CUDA cores up to the row's own position.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/dreamer.h"
+#include "common.cuh"
+#include "ops.h"
+#include "tc_common.cuh"
+
+namespace dreamer {
+namespace ops {
+namespace {
+
+struct PackedArgs {
+  const int *cu;
+  int n_seq, n_tokens, Hq, G;
+  const void *q, *k, *v;  // float32 form
+  long ldq, ldk, ldv;
+  void *out;
+  long ldo;
+  const int *out_rows;    // output row of token t, or null: t
+  float scale_log2;
+  int *err;
+};
+
+// First row and length of prompt i; boundaries outside 0 .. n_tokens or decreasing are cut.
+__device__ __forceinline__ int2 prompt_rows(const PackedArgs &a, int i) {
+  const int lo = min(max(a.cu[i], 0), a.n_tokens);
+  const int hi = min(max(a.cu[i + 1], lo), a.n_tokens);
+  return make_int2(lo, hi - lo);
+}
+
+// Item `rank` (a warp calls it): {first row, length, tile}, or tile < 0 when there are fewer items.
+// ge(p) = number of (prompt, tile) with a tile index >= p decreases in p: the item's tile index
+// is the p with ge(p + 1) <= rank < ge(p), and its prompt the (rank - ge(p + 1))-th that has
+// more than p tiles.
+template <int ROWS>
+__device__ __forceinline__ int3 find_item(const PackedArgs &a, int rank) {
+  const int lane = threadIdx.x & 31;
+  int first = 0;  // tiles of this lane's first prompt (lane): the others are read again
+  int most = 0;
+  for (int i = lane; i < a.n_seq; i += 32) {
+    const int n = (prompt_rows(a, i).y + ROWS - 1) / ROWS;
+    if (i == lane) first = n;
+    most = max(most, n);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  auto ge = [&](int p) {
+    int s = max(0, first - p);
+    for (int i = lane + 32; i < a.n_seq; i += 32)
+      s += max(0, (prompt_rows(a, i).y + ROWS - 1) / ROWS - p);
+    return __reduce_add_sync(0xffffffffu, s);
+  };
+  if (rank >= ge(0)) return make_int3(0, 0, -1);
+  int lo = 0, hi = most - 1;  // the highest p with ge(p) > rank
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (ge(mid) > rank) lo = mid;
+    else hi = mid - 1;
+  }
+  int left = rank - ge(lo + 1);
+  for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
+    const int i = i0 + lane;
+    const int2 pr = i < a.n_seq ? prompt_rows(a, i) : make_int2(0, 0);
+    const unsigned has = __ballot_sync(0xffffffffu, (pr.y + ROWS - 1) / ROWS > lo);
+    const int n = __popc(has);
+    if (left < n) {
+      const unsigned below = (1u << lane) - 1;
+      const int src = __ffs(__ballot_sync(0xffffffffu, ((has >> lane) & 1) && __popc(has & below) == left)) - 1;
+      return make_int3(__shfl_sync(0xffffffffu, pr.x, src), __shfl_sync(0xffffffffu, pr.y, src), lo);
+    }
+    left -= n;
+  }
+  return make_int3(0, 0, -1);
+}
+
+// boundaries that are not 0 <= cu[0] <= ... <= cu[n_seq] <= n_tokens are reported
+__device__ __forceinline__ void check_cu(const PackedArgs &a) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  for (int i = lane; i < a.n_seq; i += 32) bad |= a.cu[i] < 0 || a.cu[i + 1] < a.cu[i] || a.cu[i + 1] > a.n_tokens;
+  if (bad) raise_dev_error(a.err, DEV_BAD_INDEX);
+}
+
+// ---- bfloat16: tcgen05 ---------------------------------------------------------------------
+// The structure of the handle's sequence attention (tc_attn.cuh): a CTA takes one head and two
+// adjacent 128-query tiles A, B of a prompt that share every K/V block; warp 0 loads Q and K by
+// TMA, warp 2 V, warp 1 issues the MMAs, warps 3-10 hold one query row a thread.  Scores, weights
+// and outputs stay in tensor memory; the output is rescaled only when a row's maximum grows by
+// more than 2^8.  Weights enter the output product as bf16 (half a step of 2^-8 relative each, as
+// the stored output is), their sum is of the float32 values.
+template <int D>
+struct PkCfg {
+  static constexpr int CH = D / 64;                 // 64-column chunks of a head
+  static constexpr int TILE = 128 * 128;            // bytes of one [128 x 64] bf16 chunk
+  static constexpr int KST = D == 64 ? 4 : 2;       // K ring depth
+  static constexpr int VST = D == 64 ? 4 : 2;       // V ring depth
+  static constexpr int Q_BYTES = 2 * CH * TILE;     // both query tiles
+  static constexpr int KV_BYTES = CH * TILE;        // one K (or V) block
+  static constexpr int SMEM = Q_BYTES + (KST + VST) * KV_BYTES + 1024 + 256;
+  static_assert(SMEM <= 227 * 1024, "smem");
+};
+
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r) : "r"(taddr) : "memory");
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(352, 1)
+    packed_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, PackedArgs a) {
+  using namespace tc;
+  using C = PkCfg<D>;
+  constexpr int CH = C::CH, KST = C::KST, VST = C::VST;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sQ = smem;
+  uint8_t *sK = sQ + C::Q_BYTES;
+  uint8_t *sV = sK + KST * C::KV_BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sV + VST * C::KV_BYTES);
+  uint64_t *q_full = bars;
+  uint64_t *k_full = q_full + 1, *k_empty = k_full + KST;
+  uint64_t *v_full = k_empty + KST, *v_empty = v_full + VST;
+  uint64_t *s_full = v_empty + VST, *p_full = s_full + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(p_full + 2);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int *item_slot = reinterpret_cast<int *>(tmem_slot + 2);          // row0, length, tile
+  volatile int *by_rows = reinterpret_cast<volatile int *>(tmem_slot + 5);  // [2] diagonal block on CUDA cores
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x % a.Hq;
+  pdl_wait();  // inputs of the previous kernel are visible from here on
+  if (warp == 0) {
+    if (blockIdx.x == 0) check_cu(a);
+    const int3 it = find_item<256>(a, blockIdx.x / a.Hq);
+    if (lane == 0) {
+      item_slot[0] = it.x;
+      item_slot[1] = it.y;
+      item_slot[2] = it.z;
+    }
+  }
+  if (threadIdx.x == 32) {
+    mbar_init(smem_u32(q_full), 1);
+    for (int s = 0; s < KST; s++) {
+      mbar_init(smem_u32(&k_full[s]), 1);
+      mbar_init(smem_u32(&k_empty[s]), 1);
+    }
+    for (int s = 0; s < VST; s++) {
+      mbar_init(smem_u32(&v_full[s]), 1);
+      mbar_init(smem_u32(&v_empty[s]), 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 128);
+      by_rows[i] = 0;
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmq);
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+  }
+  __syncthreads();
+  const int row0 = item_slot[0], S = item_slot[1], pair = item_slot[2];
+  if (pair < 0) {  // fewer items than launched
+    pdl_trigger();
+    return;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();  // after the TMEM allocation (see pdl_trigger)
+  const int qtA = 2 * pair, qtB = 2 * pair + 1;
+  const bool hasB = qtB * 128 < S;
+  const int nbA = qtA + 1, nbB = hasB ? qtB + 1 : 0;
+  const int nb = hasB ? nbB : nbA;
+  // TMEM columns: S_A 0..127, S_B 128..255, O_A 256.., O_B 256 + D..
+  const uint32_t tS = tmem, tO = tmem + 256;
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------- producers (warp 0: Q, K; warp 2: V)
+    if (lane == 0) {
+      const bool isK = warp == 0;
+      const int colb = (head / a.G) * D;
+      if (isK) {
+        mbar_expect_tx(smem_u32(q_full), (hasB ? 2 : 1) * CH * C::TILE);
+        for (int t = 0; t < (hasB ? 2 : 1); t++)
+          for (int c = 0; c < CH; c++)
+            tma_load_2d(smem_u32(sQ + (t * CH + c) * C::TILE), &tmq, smem_u32(q_full), head * D + 64 * c,
+                        row0 + (t == 0 ? qtA : qtB) * 128);
+      }
+      const CUtensorMap *tm = isK ? &tmk : &tmv;
+      const int NS = isK ? KST : VST;
+      uint64_t *fullb = isK ? k_full : v_full, *emptyb = isK ? k_empty : v_empty;
+      uint8_t *ring = isK ? sK : sV;
+      int issued_ph[4] = {-1, -1, -1, -1};
+      bool ok = true;
+      for (int j = 0; j < nb; j++) {
+        const int s = j % NS;
+        const uint32_t ph = (j / NS) & 1;
+        if (!mbar_wait(smem_u32(&emptyb[s]), ph ^ 1, abort_flag, a.err)) { ok = false; break; }
+        mbar_expect_tx(smem_u32(&fullb[s]), C::KV_BYTES);
+        for (int c = 0; c < CH; c++)
+          tma_load_2d(smem_u32(ring + s * C::KV_BYTES + c * C::TILE), tm, smem_u32(&fullb[s]),
+                      colb + 64 * c, row0 + j * 128);
+        issued_ph[s] = (int)ph;
+      }
+      // every copy issued lands before the CTA can exit
+      const uint64_t t0 = globaltimer();
+      if (isK)
+        while (!mbar_try_wait(smem_u32(q_full), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+        }
+      if (!ok)
+        for (int i = 0; i < NS; i++)
+          if (issued_ph[i] >= 0) {
+            const uint64_t t1 = globaltimer();
+            while (!mbar_try_wait(smem_u32(&fullb[i]), (uint32_t)issued_ph[i]) &&
+                   globaltimer() - t1 < WAIT_LIMIT_NS) {
+            }
+          }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------- MMA issuer (order as in tc_attn.cuh)
+    if (lane == 0) {
+      constexpr uint32_t ID_S = idesc_bf16_m128(128);
+      constexpr uint32_t ID_PV = idesc_bf16_m128_bmn(D);
+      bool ok = mbar_wait(smem_u32(q_full), 0, abort_flag, a.err);
+      const uint32_t q0 = smem_u32(sQ);
+      auto issue_s = [&](int t, uint32_t k0) {
+        const uint32_t qt0 = q0 + t * CH * C::TILE;
+#pragma unroll
+        for (int k = 0; k < D / 16; k++) {
+          const uint32_t off = (k >> 2) * C::TILE + (k & 3) * 32;
+          mma_bf16(tS + t * 128, desc_k128(qt0 + off), desc_k128(k0 + off), ID_S, k != 0);
+        }
+      };
+      if (ok && mbar_wait(smem_u32(&k_full[0]), 0, abort_flag, a.err)) {
+        tc_fence_after();
+        const uint32_t k0 = smem_u32(sK);
+        issue_s(0, k0);
+        mma_commit(smem_u32(&s_full[0]));
+        if (nbB > 0) {
+          issue_s(1, k0);
+          mma_commit(smem_u32(&s_full[1]));
+        }
+        mma_commit(smem_u32(&k_empty[0]));
+      } else {
+        ok = false;
+      }
+      for (int j = 0; j < nb && ok; j++) {
+        const int vs = j % VST;
+        if (!mbar_wait(smem_u32(&v_full[vs]), (j / VST) & 1, abort_flag, a.err)) break;
+        tc_fence_after();
+        const uint32_t v0 = smem_u32(sV + vs * C::KV_BYTES);
+        const bool next = j + 1 < nb;
+        const int ks = (j + 1) % KST;
+        uint32_t k1 = 0;
+        if (next) {
+          if (!mbar_wait(smem_u32(&k_full[ks]), ((j + 1) / KST) & 1, abort_flag, a.err)) break;
+          tc_fence_after();
+          k1 = smem_u32(sK + ks * C::KV_BYTES);
+        }
+        for (int t = 0; t < 2; t++) {
+          const int nbt = t == 0 ? nbA : nbB;
+          if (j >= nbt) continue;
+          if (!mbar_wait(smem_u32(&p_full[t]), j & 1, abort_flag, a.err)) { ok = false; break; }
+          tc_fence_after();
+          if (!(j + 1 == nbt && by_rows[t])) {
+#pragma unroll
+            for (int k = 0; k < 8; k++)  // 128 keys, 16 per instruction (8 TMEM columns of P)
+              mma_bf16_ts(tO + t * D, tS + t * 128 + k * 8, desc_mn128(v0 + k * 2048, C::TILE), ID_PV,
+                          (j | k) != 0);
+          }
+          if (j + 1 < nbt) issue_s(t, k1);
+          mma_commit(smem_u32(&s_full[t]));
+        }
+        if (!ok) break;
+        mma_commit(smem_u32(&v_empty[vs]));
+        if (next) mma_commit(smem_u32(&k_empty[ks]));
+      }
+    }
+  } else if (warp >= 3) {
+    // ------------------------------------------------- softmax (tile A: warps 3-6, B: 7-10)
+    const int t = warp < 7 ? 0 : 1;
+    const int nbt = t == 0 ? nbA : nbB;
+    const int qt = t == 0 ? qtA : qtB;
+    if (nbt > 0) {
+      const int q = warp & 3;
+      const int row = q * 32 + lane;
+      const int qi = qt * 128 + row;               // query position in the prompt
+      const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+      const uint32_t sbuf = tS + t * 128 + lane_off;
+      const uint32_t obuf = tO + t * D + lane_off;
+      float m_ref = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nbt; j++) {
+        const bool diag = (j == qt);
+        if (diag) {
+          // the diagonal block's values: rows behind the prompt's end are cleared, and a value
+          // that is not finite sends the block's output product to the row form below
+          ok = mbar_wait(smem_u32(&v_full[j % VST]), (j / VST) & 1, abort_flag, a.err);
+          bool bad = false;
+          if (ok) {
+            uint8_t *vr = sV + (j % VST) * C::KV_BYTES + row * 128;
+            if (qi >= S) {
+#pragma unroll
+              for (int c = 0; c < CH * 8; c++)
+                *reinterpret_cast<uint4 *>(vr + (c >> 3) * C::TILE + ((c + row) & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async();
+            } else {
+              __nv_bfloat162 z = __float2bfloat162_rn(0.f), acc = z;  // x * 0 is NaN where x is not finite
+#pragma unroll
+              for (int c = 0; c < CH * 8; c++) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(vr + (c >> 3) * C::TILE + ((c + row) & 7) * 16);
+                const __nv_bfloat162 *h2 = reinterpret_cast<const __nv_bfloat162 *>(&w);
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc = __hfma2(h2[e], z, acc);
+              }
+              const uint32_t u = *reinterpret_cast<const uint32_t *>(&acc);
+              bad = (u & 0x7fff7fffu) != 0;
+            }
+          }
+          if (bad) by_rows[t] = 1;  // seen by the MMA warp through p_full, by this warp through s_full
+          if (!ok) break;
+        }
+        if (!mbar_wait(smem_u32(&s_full[t]), j & 1, abort_flag, a.err)) { ok = false; break; }
+        tc_fence_after();
+        const int lim = qi - j * 128;  // diagonal block: last visible key of the row
+        // the row's 128 scores into registers with four loads in flight
+        float sv[128];
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32_async(sbuf + c, sv + c);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld_fence(sv + c);
+        if (diag) {
+#pragma unroll
+          for (int i = 0; i < 128; i++)
+            if (i > lim) sv[i] = -INFINITY;
+        }
+        // row max of the raw scores (the scale is positive: applied to the max)
+        float mc[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int i = 4; i < 124; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; k++) mc[k] = max3f(mc[k], sv[i + 2 * k], sv[i + 2 * k + 1]);
+        mc[0] = max3f(mc[0], sv[124], sv[125]);
+        mc[1] = max3f(mc[1], sv[126], sv[127]);
+        const float mraw = max3f(mc[0], mc[1], fmaxf(mc[2], mc[3]));
+        const float mx = mraw * a.scale_log2;
+        // lazy rescale: move the reference max only when the row max grows by more than 8
+        float m_new = m_ref, alpha = 1.f;
+        if (mx > m_ref + 8.f) {
+          m_new = mx;
+          alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
+        }
+        const float m_use = m_new == -INFINITY ? 0.f : m_new;
+        // P = 2^(s * scale - m) as bf16 pairs (the lower key in the low half) into the first
+        // 64 columns of this tile's S in TMEM, where the P.V MMA reads it, and summed
+        const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-m_use, -m_use);
+        uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four independent sums of pairs
+#pragma unroll
+        for (int hh = 0; hh < 2; hh++) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; e++) {
+            const int i = hh * 64 + 2 * e;
+            const float2 x = f2_unpack(f2_fma(f2_pack(sv[i], sv[i + 1]), sc2, nm2));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            rs2[e & 3] = f2_add(rs2[e & 3], f2_pack(p0, p1));
+            w[e] = bf2_pack_rn(p0, p1);
+          }
+          tmem_st32_nowait(sbuf + hh * 32, w);
+        }
+        const float2 rsf = f2_unpack(f2_add(f2_add(rs2[0], rs2[1]), f2_add(rs2[2], rs2[3])));
+        const float rs = rsf.x + rsf.y;
+        // O rescaled before P_t(j) V accumulates into it (s_full of block j also means that
+        // P_t(j-1) V has completed; P_t(j) V is issued after p_full below)
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float ov[32];
+            tmem_ld32(obuf + c, ov);
+#pragma unroll
+            for (int i = 0; i < 32; i++) ov[i] *= alpha;
+            tmem_st32(obuf + c, ov);
+          }
+        }
+        l = l * alpha + rs;
+        m_ref = m_new;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[t]));
+      }
+      // the commit after the last P.V: O_t is final
+      if (ok && mbar_wait(smem_u32(&s_full[t]), nbt & 1, abort_flag, a.err)) {
+        tc_fence_after();
+        const float inv = 1.0f / l;
+        const bool slow = by_rows[t] != 0;
+        const uint8_t *vlast = sV + ((nbt - 1) % VST) * C::KV_BYTES;
+        const int trow = row0 + qi;
+        const bool mine = qi < S;
+        const long orow = mine && a.out_rows ? a.out_rows[trow] : trow;
+        bf16 *dst = reinterpret_cast<bf16 *>(a.out) + orow * a.ldo + head * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float ov[32];
+          __syncwarp();
+          if (!slow || nbt > 1) {
+            tmem_ld32(obuf + c, ov);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i++) ov[i] = 0.f;
+          }
+          if (slow) {  // the diagonal block, keys 0 .. row, two a step
+            const uint8_t *vc = vlast + (c >> 6) * C::TILE;
+#pragma unroll 1
+            for (int kp = 0; kp < 64; kp++) {
+              __syncwarp();
+              const uint32_t pw = tmem_ld1(sbuf + kp);
+#pragma unroll
+              for (int hf = 0; hf < 2; hf++) {
+                const int key = 2 * kp + hf;
+                if (key > row) continue;
+                const float p = __uint_as_float(hf ? pw & 0xffff0000u : pw << 16);
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                  float v8[8];
+                  load8(reinterpret_cast<const bf16 *>(vc + key * 128 + ((((c & 63) >> 3) + x) ^ (key & 7)) * 16), v8);
+#pragma unroll
+                  for (int e = 0; e < 8; e++) ov[8 * x + e] = fmaf(p, v8[e], ov[8 * x + e]);
+                }
+              }
+            }
+          }
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              float t8[8];
+#pragma unroll
+              for (int e = 0; e < 8; e++) t8[e] = ov[i + e] * inv;
+              store8(dst + c + i, t8);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- float32: CUDA cores -------------------------------------------------------------------
+// A CTA of 128 threads takes one head and 32 query rows of a prompt, keys in blocks of 64.  The
+// threads form an 8 x 16 grid: 4 rows x 4 keys of the scores and 4 rows x D / 16 columns of the
+// output each, operands in shared memory with the reduction index outermost (Q, K and the weights
+// transposed), so a step reads two or three 16-byte words for 16 or more multiply-adds.
+template <int D>
+struct F32Cfg {
+  static constexpr int BM = 32, BN = 64;
+  static constexpr int QP = BM + 4, KP = BN + 4, PP = BM + 4;  // padded row lengths
+  static constexpr int SMEM = (D * QP + D * KP + BN * D + BN * PP) * 4;
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
+  using C = F32Cfg<D>;
+  constexpr int BM = C::BM, BN = C::BN, QP = C::QP, KP = C::KP, PP = C::PP;
+  constexpr int OC = D / 16;  // output columns of a thread
+  extern __shared__ __align__(16) float fsm[];
+  float *sQ = fsm;            // [D][QP]
+  float *sK = sQ + D * QP;    // [D][KP]
+  float *sV = sK + D * KP;    // [BN][D]
+  float *sP = sV + BN * D;    // [BN][PP]
+  __shared__ int item[3];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int head = blockIdx.x % a.Hq, kvh = head / a.G;
+  if (tid < 32) {
+    if (blockIdx.x == 0) check_cu(a);
+    const int3 it = find_item<BM>(a, blockIdx.x / a.Hq);
+    if (tid == 0) {
+      item[0] = it.x;
+      item[1] = it.y;
+      item[2] = it.z;
+    }
+  }
+  __syncthreads();
+  const int row0 = item[0], S = item[1], tile = item[2];
+  if (tile < 0) return;
+  const int q0 = tile * BM;
+  const int ty = tid >> 4, tx = tid & 15;  // rows 4 ty .., keys 4 tx .., columns tx * 4 + 64 i ..
+  const float *Q = reinterpret_cast<const float *>(a.q) + (long)(row0 + q0) * a.ldq + (long)head * D;
+  for (int e = tid; e < BM * (D / 4); e += 128) {
+    const int r = e / (D / 4), c = e % (D / 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q0 + r < S) v = *reinterpret_cast<const float4 *>(Q + (long)r * a.ldq + 4 * c);
+    sQ[(4 * c) * QP + r] = v.x;
+    sQ[(4 * c + 1) * QP + r] = v.y;
+    sQ[(4 * c + 2) * QP + r] = v.z;
+    sQ[(4 * c + 3) * QP + r] = v.w;
+  }
+  float o[4][OC], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < OC; c++) o[i][c] = 0.f;
+  }
+  const int last = min(S, q0 + BM);  // keys of the tile's last row
+  for (int k0 = 0; k0 < last; k0 += BN) {
+    __syncthreads();
+    const float *K = reinterpret_cast<const float *>(a.k) + (long)(row0 + k0) * a.ldk + (long)kvh * D;
+    const float *V = reinterpret_cast<const float *>(a.v) + (long)(row0 + k0) * a.ldv + (long)kvh * D;
+    for (int e = tid; e < BN * (D / 4); e += 128) {
+      const int r = e / (D / 4), c = e % (D / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+      if (k0 + r < S) {
+        v = *reinterpret_cast<const float4 *>(K + (long)r * a.ldk + 4 * c);
+        w = *reinterpret_cast<const float4 *>(V + (long)r * a.ldv + 4 * c);
+      }
+      sK[(4 * c) * KP + r] = v.x;
+      sK[(4 * c + 1) * KP + r] = v.y;
+      sK[(4 * c + 2) * KP + r] = v.z;
+      sK[(4 * c + 3) * KP + r] = v.w;
+      *reinterpret_cast<float4 *>(sV + r * D + 4 * c) = w;
+    }
+    __syncthreads();
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) s[i][j] = 0.f;
+#pragma unroll 8
+    for (int d = 0; d < D; d++) {
+      const float4 qv = *reinterpret_cast<const float4 *>(sQ + d * QP + 4 * ty);
+      const float4 kv = *reinterpret_cast<const float4 *>(sK + d * KP + 4 * tx);
+      const float qa[4] = {qv.x, qv.y, qv.z, qv.w}, ka[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) s[i][j] = fmaf(qa[i], ka[j], s[i][j]);
+    }
+    const bool diag = k0 + BN > q0;  // some key of the block is behind some row
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        s[i][j] *= a.scale_log2;
+        if (diag && k0 + 4 * tx + j > q0 + 4 * ty + i) s[i][j] = -INFINITY;
+        mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int k = 1; k < 16; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+      const float mn = fmaxf(m[i], mx);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float alpha = m[i] == -INFINITY ? 0.f : exp2f(m[i] - base);
+      float ps = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        s[i][j] = exp2f(s[i][j] - base);
+        ps += s[i][j];
+        sP[(4 * tx + j) * PP + 4 * ty + i] = s[i][j];
+      }
+      if (mn != m[i]) {
+        l[i] *= alpha;
+#pragma unroll
+        for (int c = 0; c < OC; c++) o[i][c] *= alpha;
+      }
+      l[i] += ps;
+      m[i] = mn;
+    }
+    __syncwarp();  // a row's weights are written and read by the same half warp
+    const int nk = min(BN, last - k0);
+    auto out_step = [&](int k, auto dtag) {
+      constexpr bool DIAG = decltype(dtag)::value;
+      const float4 pv = *reinterpret_cast<const float4 *>(sP + k * PP + 4 * ty);
+      const float pa[4] = {pv.x, pv.y, pv.z, pv.w};
+      float va[OC];
+      if constexpr (OC >= 4) {
+#pragma unroll
+        for (int c = 0; c < OC / 4; c++) {
+          const float4 w = *reinterpret_cast<const float4 *>(sV + k * D + c * 64 + 4 * tx);
+          va[4 * c] = w.x; va[4 * c + 1] = w.y; va[4 * c + 2] = w.z; va[4 * c + 3] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < OC; c++) va[c] = sV[k * D + OC * tx + c];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if (DIAG && k0 + k > q0 + 4 * ty + i) continue;  // 0 x infinity stays out
+#pragma unroll
+        for (int c = 0; c < OC; c++) o[i][c] = fmaf(pa[i], va[c], o[i][c]);
+      }
+    };
+    if (!diag) {
+#pragma unroll 8
+      for (int k = 0; k < BN; k++) out_step(k, std::false_type());
+    } else {
+#pragma unroll 2
+      for (int k = 0; k < nk; k++) out_step(k, std::true_type());
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+#pragma unroll
+    for (int k = 1; k < 16; k <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
+    const int r = q0 + 4 * ty + i;
+    if (r >= S) continue;
+    const long orow = a.out_rows ? a.out_rows[row0 + r] : row0 + r;
+    float *dst = reinterpret_cast<float *>(a.out) + orow * a.ldo + (long)head * D;
+    const float inv = 1.0f / l[i];
+    if constexpr (OC >= 4) {
+#pragma unroll
+      for (int c = 0; c < OC / 4; c++)
+        *reinterpret_cast<float4 *>(dst + c * 64 + 4 * tx) = make_float4(
+            o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
+    } else {
+#pragma unroll
+      for (int c = 0; c < OC; c++) dst[OC * tx + c] = o[i][c] * inv;
+    }
+  }
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeTiled)f;
+  }();
+  return fn;
+}
+
+// rows of 16-bit values in boxes of 128 rows x 64 columns, 128-byte swizzle; rows past the end read 0
+bool row_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, long ld) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, 128};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K, typename... A>
+int launch_packed(K kern, long items, int threads, int smem, cudaStream_t s, LaunchOpt o, const A &...args) {
+  if (items > 0x7fffffffL) return DREAMER_ERR_UNSUPPORTED;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return DREAMER_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)items);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = o.pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DREAMER_OK : DREAMER_ERR_CUDA;
+}
+
+// the most row tiles that n_tokens rows in n_seq prompts can make
+long most_tiles(long n_tokens, long n_seq, long rows) {
+  const long full = n_seq < n_tokens ? n_seq : n_tokens;  // prompts with a row
+  return (n_tokens + full * (rows - 1)) / rows;
+}
+
+}  // namespace
+
+int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
+  PackedArgs a{};
+  a.cu = p.cu; a.n_seq = p.n_seq; a.n_tokens = p.n_tokens; a.Hq = p.Hq; a.G = p.Hq / p.Hkv;
+  a.q = p.q; a.k = p.k; a.v = p.v; a.ldq = p.ldq; a.ldk = p.ldk; a.ldv = p.ldv;
+  a.out = p.out; a.ldo = p.ldo; a.out_rows = p.out_rows;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.err = p.err;
+  if (p.n_tokens == 0 || p.n_seq == 0) return DREAMER_OK;
+  if (p.dtype == 1) {
+    CUtensorMap tq, tk, tv;
+    if (!row_map(&tq, p.q, (uint64_t)p.Hq * p.d, p.n_tokens, p.ldq) ||
+        !row_map(&tk, p.k, (uint64_t)p.Hkv * p.d, p.n_tokens, p.ldk) ||
+        !row_map(&tv, p.v, (uint64_t)p.Hkv * p.d, p.n_tokens, p.ldv))
+      return DREAMER_ERR_CUDA;
+    const long items = most_tiles(p.n_tokens, p.n_seq, 256) * p.Hq;
+    if (p.d == 64) return launch_packed(packed_tc_kernel<64>, items, 352, PkCfg<64>::SMEM, s, o, tq, tk, tv, a);
+    return launch_packed(packed_tc_kernel<128>, items, 352, PkCfg<128>::SMEM, s, o, tq, tk, tv, a);
+  }
+  const long items = most_tiles(p.n_tokens, p.n_seq, 32) * p.Hq;
+  switch (p.d) {
+    case 16: return launch_packed(packed_f32_kernel<16>, items, 128, F32Cfg<16>::SMEM, s, o, a);
+    case 32: return launch_packed(packed_f32_kernel<32>, items, 128, F32Cfg<32>::SMEM, s, o, a);
+    case 64: return launch_packed(packed_f32_kernel<64>, items, 128, F32Cfg<64>::SMEM, s, o, a);
+    default: return launch_packed(packed_f32_kernel<128>, items, 128, F32Cfg<128>::SMEM, s, o, a);
+  }
+}
+
+}  // namespace ops
+}  // namespace dreamer
+
+using namespace dreamer;
+
+extern "C" int dreamer_attn_packed(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                                   int64_t ldv, void *out, int64_t ldo, const int32_t *cu_seqlens, int n_seq,
+                                   int n_tokens, int n_heads, int n_kv_heads, int head_dim, int dtype,
+                                   float scale, int32_t *status, dreamer_stream stream) {
+  if (!q || !k || !v || !out || !cu_seqlens || n_seq < 0 || n_tokens < 0) return DREAMER_ERR_ARG;
+  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || head_dim < 1) return DREAMER_ERR_ARG;
+  if ((dtype != 0 && dtype != 1) || !(scale > 0.f) || !isfinite(scale)) return DREAMER_ERR_ARG;
+  if (head_dim != 64 && head_dim != 128 && (dtype == 1 || (head_dim != 16 && head_dim != 32)))
+    return DREAMER_ERR_UNSUPPORTED;
+  const int es = dtype == 0 ? 4 : 2;
+  const void *ptr[4] = {q, k, v, out};
+  const int64_t ld[4] = {ldq, ldk, ldv, ldo};
+  for (int i = 0; i < 4; i++) {
+    const int64_t w = (int64_t)(i == 0 || i == 3 ? n_heads : n_kv_heads) * head_dim;
+    if (((uintptr_t)ptr[i] & 15) || ld[i] < w || (ld[i] * es) % 16 || ld[i] * es >= (1LL << 40)) return DREAMER_ERR_ARG;
+  }
+  ops::PackedAttn p{q, ldq, k, ldk, v, ldv, out, ldo, cu_seqlens, n_seq, n_tokens, n_heads, n_kv_heads,
+                    head_dim, dtype, scale, nullptr, status};
+  return ops::attn_packed(p, (cudaStream_t)stream);
+}

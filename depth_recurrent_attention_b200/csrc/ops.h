@@ -14,6 +14,26 @@ struct LaunchOpt {
   bool pdl = false;
 };
 
+// ---- causal attention over packed prompts -------------------------------------------------
+struct PackedAttn {
+  const void *q;
+  long ldq;  // row strides in elements; head j at column j * d
+  const void *k;
+  long ldk;
+  const void *v;
+  long ldv;
+  void *out;
+  long ldo;
+  const int *cu;  // [n_seq + 1] rows of prompt i: cu[i] .. cu[i + 1] - 1
+  int n_seq, n_tokens;
+  int Hq, Hkv, d;
+  int dtype;  // 0 float32, 1 bfloat16
+  float scale;
+  const int *out_rows;  // output row of token t, or null: t
+  int *err;             // device error flag or null
+};
+int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o = LaunchOpt());
+
 // ---- 4-bit cache: one depth of one handle, or a caller's cache --------------------------
 constexpr int KV4_BLOCK = 64;  // tokens of a block
 constexpr int KV4_GROUP = 64;  // channels that share a (scale, offset) pair

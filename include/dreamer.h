@@ -217,6 +217,25 @@ int dreamer_bias_update_counts(dreamer_handle *h, float lambda, const int32_t *c
 int dreamer_route_balance(dreamer_handle *h, int depth, float *lorenz, float *gini,
                           dreamer_stream stream);
 
+/* ---- Causal attention over packed prompts ---------------------------------------------------
+ * Needs no handle and allocates nothing.  The rows of n_seq prompts of different lengths lie one
+ * behind the other: prompt i holds rows cu_seqlens[i] .. cu_seqlens[i+1]-1 (int32 [n_seq+1],
+ * device, not decreasing, within 0 .. n_tokens; prompts may be empty).  A token attends its
+ * prompt's tokens up to itself; query head j uses key head j / (n_heads / n_kv_heads):
+ *   out[t] = sum_{i <= t} softmax_i(scale q[t] . k[i]) v[i].
+ * q, out: n_tokens rows of n_heads * head_dim, k, v: of n_kv_heads * head_dim, of dtype (0 =
+ * float32, 1 = bfloat16), at strides ld* (elements, a multiple of 16 bytes), 16-byte aligned.
+ * out must not overlap q, k or v.  scale > 0.  Rows of no prompt are neither used nor written.
+ * bfloat16: head_dim 64 or 128, tensor cores with float32 sums and softmax, weights of the
+ * output product rounded to bfloat16.  float32: head_dim 16, 32, 64 or 128, CUDA cores.
+ * `status` is NULL or a device int32 that the caller clears: set non-zero by boundaries that are
+ * not as above (their prompts are cut) or by an expired bounded wait.  Asynchronous on `stream`,
+ * on the current device.                                                                    */
+int dreamer_attn_packed(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                        int64_t ldv, void *out, int64_t ldo, const int32_t *cu_seqlens, int n_seq,
+                        int n_tokens, int n_heads, int n_kv_heads, int head_dim, int dtype,
+                        float scale, int32_t *status, dreamer_stream stream);
+
 /* ---- A 4-bit cache of attention keys and values ---------------------------------------------
  * These entry points need no handle and allocate nothing.  A group is 64 consecutive channels
  * of one head of one token: s = (max - min) / 15 and m = min, both rounded to bfloat16,

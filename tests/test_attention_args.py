@@ -82,3 +82,35 @@ def test_the_binding_refuses_tensors_of_the_host():
         KV4Cache.alloc(1, 1, 96, 64)
     with pytest.raises(ValueError):
         KV4Cache.alloc(0, 1, 64, 64)
+
+
+# q ldq k ldk v ldv out ldo cu n_seq n_tokens Hq Hkv d dtype scale status stream
+PACKED = [P, 256, P, 128, P, 128, P, 256, P, 2, 10, 4, 2, 64, 1, 0.125, None, None]
+
+
+@pytest.mark.parametrize("at,value,rc", [
+    (0, None, ARG), (2, None, ARG), (4, None, ARG), (6, None, ARG), (8, None, ARG), (0, P + 8, ARG),
+    (1, 255, ARG), (1, 260, ARG), (3, 127, ARG), (5, 64, ARG), (7, 128, ARG), (1, 1 << 40, ARG),
+    (9, -1, ARG), (10, -1, ARG), (11, 3, ARG), (11, 0, ARG), (12, 0, ARG), (13, 0, ARG), (14, 2, ARG),
+    (15, 0.0, ARG), (15, -1.0, ARG), (15, float("nan"), ARG), (15, float("inf"), ARG),
+    (13, 32, UNS), (13, 96, UNS), (13, 256, UNS),
+])
+def test_packed_calls_that_are_refused(L, at, value, rc):
+    a = list(PACKED)
+    a[at] = value
+    assert L.dreamer_attn_packed(*a) == rc
+
+
+def test_packed_without_rows_or_prompts_is_no_work(L):
+    for at in (9, 10):
+        a = list(PACKED)
+        a[at] = 0
+        assert L.dreamer_attn_packed(*a) == 0
+
+
+def test_the_packed_binding_refuses_tensors_of_the_host():
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    x = torch.zeros((4, 1, 64))
+    with pytest.raises(ValueError):
+        attn_packed(x, x, x, torch.zeros(2, dtype=torch.int32))
