@@ -13,16 +13,11 @@ import math
 
 import torch
 
-from .dreamer import _check, lib
+from .dreamer import KV4CacheC, _check, lib
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 BLOCK = 64  # tokens of a cache block
 GROUP = 64  # channels that share a scale and an offset
-
-
-class KV4CacheC(C.Structure):
-    _fields_ = [("data", C.c_void_p)] + [(n, C.c_int) for n in (
-        "batch", "n_kv_heads", "head_dim", "capacity")]
 
 
 _fns = None

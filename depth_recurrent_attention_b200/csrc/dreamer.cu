@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "kernels_simt.cuh"
 #include "attn_rows.cuh"
+#include "ops.h"
 
 using namespace dreamer;
 
@@ -50,6 +51,7 @@ struct dreamer_handle {
   void *Ybuf = nullptr;          // [T k + 128][h] expert outputs in sorted order
   int *pcnt = nullptr, *poffs = nullptr, *ptiles_a = nullptr, *ptiles_b = nullptr;
   int *pcursor = nullptr, *prows = nullptr, *pinv = nullptr;
+  int *pos = nullptr;            // [T] positions of packed prompts' tokens
   int *err = nullptr;
   void *k3 = nullptr;            // [E][3 d_r] bf16: router keys repeated for split scores
   void *kEt = nullptr;           // [d_r][E] bf16: router keys transposed (CUDA-core scores)
@@ -71,7 +73,7 @@ struct dreamer_handle {
   int use_pdl = 1;               // programmatic dependent launch between kernels of a stream
   bool pdl_ok[3] = {false, false, false};  // main / side / side2: the last operation was a kernel
   struct GraphEntry {
-    int kind;                    // 0 forward, 1 decode
+    int kind;                    // 0 forward, 1 decode, 2 decode over a 4-bit cache, 3 packed forward
     const void *key[5];
     int l0, l1, prof;
     int captured;                // 0: seen once (ran directly), 1: graph ready
@@ -477,6 +479,7 @@ extern "C" int dreamer_init(const dreamer_config *cfg, const dreamer_weights *w,
     DALLOC(h->ptiles_b, (G + 1) * sizeof(int));
     DALLOC(h->prows, T * sizeof(int));
     DALLOC(h->pinv, T * sizeof(int));
+    DALLOC(h->pos, T * sizeof(int));
     DALLOC(h->err, sizeof(int));
     if (c.max_cache_len > 0) {
       // key ranges per (sequence, head): about ten waves of three CTAs per SM, at least 16
@@ -726,11 +729,11 @@ static void launch_rows(dreamer_handle *h, const RowsArgs &a, int d, cudaStream_
 // SA_FLOPS_SM_D64 flop/s an SM.  0 when the split does not pay (DA then runs at full width).
 static constexpr double DA_BYTES_SM = 26e9, DA_BYTES_ALL = 4.7e12;
 static constexpr double SA_FLOPS_SM_D128 = 5.3e12, SA_FLOPS_SM_D64 = 2.5e12;
-static int da_beside_sa_sms(const dreamer_handle *h, int l, int r0) {
+static int da_beside_sa_sms(const dreamer_handle *h, int l, int r0, double n_prompts, double len) {
   const dreamer_config &c = h->cfg;
-  const double hd = c.hidden, T = (double)c.batch * c.seq;
+  const double hd = c.hidden, T = n_prompts * len;
   const double bytes = T * (double)(l + 1 - r0) * 4.0 * hd;  // the depths' bf16 K and V rows
-  const double flops = 2.0 * hd * c.batch * (double)c.seq * (c.seq + 1.0);  // causal half
+  const double flops = 2.0 * hd * n_prompts * len * (len + 1.0);  // causal half
   const double r_sa = c.head_dim == 128 ? SA_FLOPS_SM_D128 : SA_FLOPS_SM_D64;
   const int S = h->num_sms;
   double best = 1e30;
@@ -829,7 +832,7 @@ static void trace_next(dreamer_handle *h, const dreamer_trace *tr, int l, int n,
 }
 
 struct DepthIO {
-  int mode;               // 0 prefill, 1 decode
+  int mode;               // 0 prefill, 1 decode, 2 decode over a 4-bit cache, 3 packed prefill
   int n_tok;
   const void *x_in;       // first depth only
   void *x_out;            // written by the last depth's combine
@@ -837,6 +840,9 @@ struct DepthIO {
   void *da_kv;
   void *k_cache, *v_cache;
   const int *cache_len;
+  dreamer_kv4_cache kv4;  // mode 2: all depths, one behind the other
+  const int *cu;          // mode 3: [n_seq + 1] prompt boundaries
+  int n_seq;
 };
 
 // One depth step for all n_tok tokens.
@@ -922,7 +928,8 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
   // rows, so that the O projection reads them in order too.
   const int *prow = nullptr;
   const float *psig = nullptr;
-  const bool sorted = P > 0 && tc && io.mode == 0 && c.variant != 1;
+  const bool prefill = io.mode == 0 || io.mode == 3;
+  const bool sorted = P > 0 && tc && prefill && c.variant != 1;
   if (P > 0) {
     mark(h, s, DREAMER_STAGE_PROJ_ROUTE);
     // pcnt / pcursor are zero here: cleared at init and by every depth's combine kernel
@@ -962,6 +969,11 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
   eq.qkv_sa = (T *)h->qkv_sa; eq.q_da = (T *)h->q_da; eq.da_kv = (T *)io.da_kv;
   eq.k_cache = (T *)io.k_cache; eq.v_cache = (T *)io.v_cache; eq.cache_len = io.cache_len;
   eq.B = c.batch; eq.cap = c.max_cache_len; eq.err = h->err;
+  if (io.mode >= 2) {  // positions given, keys and values left in qkv_sa
+    eq.mode = 2;
+    eq.cache_len = io.mode == 2 ? io.cache_len : h->pos;
+    if (io.mode == 3) eq.cap = h->max_pos + 1;
+  }
 
   RowsArgs da{};
   da.mode = 0; da.n_q = n; da.H = c.n_heads; da.h = hd; da.L = L; da.l = l;
@@ -986,6 +998,39 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
   auto run_sa = [&](cudaStream_t st) {
     if (io.mode == 1) {
       launch_rows<T>(h, sd, d, st);
+      return;
+    }
+    const T *kv = (const T *)h->qkv_sa + hd;
+    if (io.mode == 2) {  // the new rows into the 4-bit cache, then attention over it
+      const long depth_bytes =
+          (long)dreamer_kv4_bytes(io.kv4.batch, io.kv4.n_kv_heads, io.kv4.head_dim, io.kv4.capacity);
+      const ops::Kv4Cache c4{(uint8_t *)io.kv4.data + l * depth_bytes, c.batch, c.n_heads, d, io.kv4.capacity};
+      ops::Kv4Rows r4{};
+      r4.k = kv; r4.v = kv + hd; r4.ldk = r4.ldv = 3 * hd;
+      r4.start = io.cache_len; r4.n_rows = n; r4.dtype = c.dtype; r4.err = h->err;
+      ops::Kv4Attn a4{};
+      a4.q = h->qkv_sa; a4.ldq = 3 * hd; a4.out = h->attn; a4.ldo = 2 * hd;
+      a4.lens = io.cache_len; a4.len_add = 1; a4.Hq = c.n_heads; a4.dtype = c.dtype;
+      a4.scale = 1.0f / sqrtf((float)d); a4.err = h->err;
+      ops::LaunchOpt o;
+      o.pdl = pdl_take(h, st);
+      if (ops::kv4_store(c4, r4, st, o) != DREAMER_OK) h->path_err = 1;
+      o.pdl = pdl_take(h, st);
+      if (ops::kv4_attn(c4, a4, st, o) != DREAMER_OK) h->path_err = 1;
+      g_launches += 2;
+      return;
+    }
+    if (io.mode == 3) {
+      ops::PackedAttn pa{};
+      pa.q = h->qkv_sa; pa.k = kv; pa.v = kv + hd; pa.ldq = pa.ldk = pa.ldv = 3 * hd;
+      pa.out = h->attn; pa.ldo = 2 * hd; pa.cu = io.cu; pa.n_seq = io.n_seq; pa.n_tokens = n;
+      pa.Hq = pa.Hkv = c.n_heads; pa.d = d; pa.dtype = c.dtype; pa.scale = 1.0f / sqrtf((float)d);
+      pa.out_rows = sorted ? h->pinv : nullptr; pa.err = h->err;
+      ops::LaunchOpt o;
+      o.pdl = pdl_take(h, st);
+      if (ops::attn_packed(pa, st, o) != DREAMER_OK) h->path_err = 1;
+      ++g_launches;
+      ++(tc ? g_launches_tc : g_launches_simt);
       return;
     }
     if (!tc)
@@ -1052,7 +1097,8 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
     // on the side stream beside SA (two branches of the captured graph), on SMs of its own
     // where that pays; with stage profiling on they run one after the other (same launch
     // shapes) so each stage's time is its own.
-    const int da_sms = io.mode == 0 && c.dtype == 1 ? da_beside_sa_sms(h, l, da.r0) : 0;
+    const double prompts = io.mode == 3 ? io.n_seq : c.batch;  // packed: of their mean length
+    const int da_sms = prefill && c.dtype == 1 ? da_beside_sa_sms(h, l, da.r0, prompts, n / prompts) : 0;
     if (h->prof) {
       mark(h, s, DREAMER_STAGE_DA);
       launch_rows<T>(h, da, d, s, da_sms);
@@ -1083,7 +1129,7 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
     pdl_break(h, s);
   }
   // per-depth dumps (before the combine replaces x^ with the next depth's)
-  trace_depth(h, io.tr, l, n, io.mode == 0, s);
+  trace_depth(h, io.tr, l, n, prefill, s);
   // 8. x_{l+1} = y + sum_s w_s Y_s, then the next depth's RMSNorm (or the call's output)
   mark(h, s, DREAMER_STAGE_FINISH);
   if (c.dtype == 1) {  // bf16: a CTA of h / 8 threads per token (h <= 4096, k <= 16)
@@ -1226,11 +1272,34 @@ static int run_graphed(dreamer_handle *h, int kind, const void *const key[5], in
   return DREAMER_OK;
 }
 
+// positions of packed prompts' tokens: token t of prompt i is at t - cu[i].  Boundaries that are
+// not 0 = cu[0] <= ... <= cu[n_seq] = n_tok, and prompts longer than the RoPE table, are reported.
+__global__ void packed_pos_kernel(const int *cu, int n_seq, int n_tok, int max_len, int *pos, int *err) {
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  for (int i = t; i < n_seq; i += gridDim.x * blockDim.x) {
+    const int a = cu[i], b = cu[i + 1];
+    if (a < 0 || b < a || b > n_tok || b - a > max_len || (i == 0 && a != 0) || (i == n_seq - 1 && b != n_tok))
+      raise_dev_error(err, DEV_BAD_INDEX);
+  }
+  if (t >= n_tok) return;
+  int lo = 0, hi = n_seq;  // first prompt whose end lies past t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid + 1] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  const int p = lo < n_seq ? t - cu[lo] : 0;
+  pos[t] = p < 0 || p > max_len ? 0 : p;  // out of range only where it was reported
+}
+
 template <typename T>
 static int forward_impl(dreamer_handle *h, const void *x_in, void *x_out, int l0, int l1,
-                        void *da_kv, const dreamer_trace *tr, cudaStream_t s) {
+                        void *da_kv, const dreamer_trace *tr, cudaStream_t s,
+                        const int *cu = nullptr, int n_seq = 0, int n_packed = 0) {
   const dreamer_config &c = h->cfg;
-  const int n = c.batch * c.seq;
+  const int n = cu ? n_packed : c.batch * c.seq;
   CK(cudaMemsetAsync(h->counts, 0, (size_t)c.depth * c.n_experts * sizeof(int), s));
   // grouping counters: zero between depths by construction; cleared here as well so that a
   // call after a failed one starts clean
@@ -1240,9 +1309,13 @@ static int forward_impl(dreamer_handle *h, const void *x_in, void *x_out, int l0
   pdl_break(h, h->side);
   pdl_break(h, h->side2);
   DepthIO io{};
-  io.mode = 0; io.n_tok = n; io.x_in = x_in; io.x_out = x_out; io.tr = tr;
+  io.mode = cu ? 3 : 0; io.n_tok = n; io.x_in = x_in; io.x_out = x_out; io.tr = tr;
   io.da_kv = da_kv ? da_kv : h->da_kv_int;
+  io.cu = cu; io.n_seq = n_seq;
   h->path_err = 0;
+  if (cu)
+    launch_k(h, packed_pos_kernel, dim3(cdiv(n, 256)), dim3(256), 0, s, cu, n_seq, n, h->max_pos + 1, h->pos,
+             h->err);
   for (int l = l0; l < l1; l++) run_depth<T>(h, l, l == l0, l == l1 - 1, io, s);
   if (h->path_err) return DREAMER_ERR_UNSUPPORTED;
   if (l1 == l0 && x_out != x_in) {
@@ -1286,7 +1359,8 @@ extern "C" int dreamer_core_forward(dreamer_handle *h, const void *x_in, void *x
 
 template <typename T>
 static int decode_impl(dreamer_handle *h, const void *x_new, void *kc, void *vc,
-                       const int32_t *len, void *x_out, const dreamer_trace *tr, cudaStream_t s) {
+                       const int32_t *len, void *x_out, const dreamer_trace *tr, cudaStream_t s,
+                       const dreamer_kv4_cache *kv4 = nullptr) {
   const dreamer_config &c = h->cfg;
   const int n = c.batch;
   CK(cudaMemsetAsync(h->counts, 0, (size_t)c.depth * c.n_experts * sizeof(int), s));
@@ -1298,8 +1372,9 @@ static int decode_impl(dreamer_handle *h, const void *x_new, void *kc, void *vc,
   pdl_break(h, h->side);
   pdl_break(h, h->side2);
   DepthIO io{};
-  io.mode = 1; io.n_tok = n; io.x_in = x_new; io.x_out = x_out; io.tr = tr;
+  io.mode = kv4 ? 2 : 1; io.n_tok = n; io.x_in = x_new; io.x_out = x_out; io.tr = tr;
   io.da_kv = h->da_kv_int;
+  if (kv4) io.kv4 = *kv4;
   io.k_cache = kc; io.v_cache = vc; io.cache_len = len;
   h->path_err = 0;
   for (int l = 0; l < c.depth; l++) run_depth<T>(h, l, l == 0, l == c.depth - 1, io, s);
@@ -1332,6 +1407,74 @@ extern "C" int dreamer_decode_step(dreamer_handle *h, const void *x_new, void *k
   } else {
     const void *key[5] = {x_new, k_cache, v_cache, cache_len, x_out};
     rc = run_graphed(h, 1, key, 0, h->cfg.depth, s, enqueue);
+  }
+  h->launches += g_launches - l0c;
+  h->launches_tc += g_launches_tc - l0tc;
+  h->launches_simt += g_launches_simt - l0simt;
+  return rc;
+}
+
+extern "C" int dreamer_core_forward_packed(dreamer_handle *h, const void *x_in, void *x_out,
+                                           const int32_t *cu_seqlens, int n_seq, int n_tokens,
+                                           int depth_begin, int depth_end, void *da_kv,
+                                           const dreamer_trace *trace, dreamer_stream stream) {
+  if (!h || !x_in || !x_out || !cu_seqlens) return DREAMER_ERR_ARG;
+  const dreamer_config &c = h->cfg;
+  if (n_tokens < 1 || n_tokens > h->T || n_seq < 1) return DREAMER_ERR_ARG;
+  if (depth_begin < 0 || depth_end > c.depth || depth_begin > depth_end) return DREAMER_ERR_ARG;
+  if (!da_kv && depth_begin != 0 && c.variant != 3) return DREAMER_ERR_ARG;
+  if (!aligned16(x_in) || !aligned16(x_out) || (da_kv && !aligned16(da_kv))) return DREAMER_ERR_ARG;
+  int e = check_dev_error(h);
+  if (e) return e;
+  cudaStream_t s = (cudaStream_t)stream;
+  auto enqueue = [&]() -> int {
+    return c.dtype == 0 ? forward_impl<float>(h, x_in, x_out, depth_begin, depth_end, da_kv, trace, s,
+                                              cu_seqlens, n_seq, n_tokens)
+                        : forward_impl<bf16>(h, x_in, x_out, depth_begin, depth_end, da_kv, trace, s,
+                                             cu_seqlens, n_seq, n_tokens);
+  };
+  const uint64_t l0c = g_launches, l0tc = g_launches_tc, l0simt = g_launches_simt;
+  int rc;
+  if (trace) {
+    rc = enqueue();
+  } else {
+    const void *key[5] = {x_in, x_out, da_kv, cu_seqlens,
+                          (const void *)(((uintptr_t)(uint32_t)n_seq << 32) | (uint32_t)n_tokens)};
+    rc = run_graphed(h, 3, key, depth_begin, depth_end, s, enqueue);
+  }
+  h->launches += g_launches - l0c;
+  h->launches_tc += g_launches_tc - l0tc;
+  h->launches_simt += g_launches_simt - l0simt;
+  return rc;
+}
+
+extern "C" int dreamer_decode_step_kv4(dreamer_handle *h, const void *x_new, const dreamer_kv4_cache *cache,
+                                       const int32_t *cache_len, void *x_out, const dreamer_trace *trace,
+                                       dreamer_stream stream) {
+  if (!h || !x_new || !cache || !cache->data || !cache_len || !x_out) return DREAMER_ERR_ARG;
+  const dreamer_config &c = h->cfg;
+  if (c.max_cache_len < 1) return DREAMER_ERR_STATE;
+  if (cache->batch != c.batch || cache->n_kv_heads != c.n_heads || cache->head_dim != c.head_dim ||
+      cache->capacity < c.max_cache_len)
+    return DREAMER_ERR_ARG;
+  if (!dreamer_kv4_bytes(cache->batch, cache->n_kv_heads, cache->head_dim, cache->capacity))
+    return DREAMER_ERR_UNSUPPORTED;
+  if (!aligned16(x_new) || !aligned16(cache->data) || !aligned16(x_out)) return DREAMER_ERR_ARG;
+  int e = check_dev_error(h);
+  if (e) return e;
+  cudaStream_t s = (cudaStream_t)stream;
+  auto enqueue = [&]() -> int {
+    return c.dtype == 0
+               ? decode_impl<float>(h, x_new, nullptr, nullptr, cache_len, x_out, trace, s, cache)
+               : decode_impl<bf16>(h, x_new, nullptr, nullptr, cache_len, x_out, trace, s, cache);
+  };
+  const uint64_t l0c = g_launches, l0tc = g_launches_tc, l0simt = g_launches_simt;
+  int rc;
+  if (trace) {
+    rc = enqueue();
+  } else {
+    const void *key[5] = {x_new, cache->data, (const void *)(uintptr_t)cache->capacity, cache_len, x_out};
+    rc = run_graphed(h, 2, key, 0, c.depth, s, enqueue);
   }
   h->launches += g_launches - l0c;
   h->launches_tc += g_launches_tc - l0tc;

@@ -24,7 +24,8 @@ namespace dreamer {
 // unperm() maps a computed column back to its head column.
 template <typename T> struct EpiQKV {
   int h, d, L, l, S;
-  int mode;                  // 0 prefill (position = token % S), 1 decode (position = cache_len[b])
+  int mode;                  // 0 prefill (position = token % S), 1 decode (position = cache_len[b]),
+                             // 2 position = cache_len[token], keys and values kept in qkv_sa
   int col_lo;                // first column of the fused projection this GEMM computes
   int perm;                  // q_SA / k_SA column order as above
   const float *psig;         // [T] or null (dense)
@@ -34,8 +35,8 @@ template <typename T> struct EpiQKV {
   T *q_da;                   // [T][h]
   T *da_kv;                  // [T][L][2][h]
   T *k_cache, *v_cache;      // decode: [L][B][H][cap][d]
-  const int *cache_len;      // decode: [B]
-  int B, cap;
+  const int *cache_len;      // mode 1: [B], mode 2: [T]
+  int B, cap;                // positions from cap on are refused
   int *err;                  // device error flag
 
   __device__ __forceinline__ static int unperm(int c) {  // c in [0, 128)
@@ -48,7 +49,7 @@ template <typename T> struct EpiQKV {
   __device__ __forceinline__ T *dest(int token, int nc) const {
     const int blk = nc / h, head = (nc % h) / d, hc = nc % h;
     if (blk <= 2) {
-      if (mode == 0 || blk == 0) return qkv_sa + (long)token * 3 * h + blk * h + hc;
+      if (mode != 1 || blk == 0) return qkv_sa + (long)token * 3 * h + blk * h + hc;
       const int pos = cache_len[token];
       if (pos < 0 || pos >= cap) return nullptr;
       T *base = (blk == 1) ? k_cache : v_cache;
@@ -227,7 +228,7 @@ template <typename T> struct EpiQKV {
         v[i + 32] = t;
       }
     }
-    if (mode == 1 && blk <= 2 && position(token) < 0) {  // slot outside the cache
+    if (mode != 0 && blk <= 2 && position(token) < 0) {  // slot outside the cache
       raise_dev_error(err, DEV_BAD_INDEX);
       return;
     }

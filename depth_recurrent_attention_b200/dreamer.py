@@ -52,6 +52,11 @@ STAGES = ("norm", "proj_route", "qkv", "da", "sa", "o_proj", "ea_route", "permut
           "experts", "finish")
 
 
+class KV4CacheC(C.Structure):
+    _fields_ = [("data", C.c_void_p)] + [(n, C.c_int) for n in (
+        "batch", "n_kv_heads", "head_dim", "capacity")]
+
+
 class StatsC(C.Structure):
     _fields_ = [("launches", C.c_uint64), ("ms", C.c_double * len(STAGES)),
                 ("count", C.c_uint64 * len(STAGES)), ("launches_tc", C.c_uint64),
@@ -74,6 +79,8 @@ def lib(path: str = LIB_PATH):
         L.dreamer_init.argtypes = [C.POINTER(ConfigC), C.POINTER(WeightsC), vp, C.POINTER(vp)]
         L.dreamer_core_forward.argtypes = [vp, vp, vp, i, i, vp, vp, vp]
         L.dreamer_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+        L.dreamer_core_forward_packed.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, vp, vp]
+        L.dreamer_decode_step_kv4.argtypes = [vp, vp, vp, vp, vp, vp, vp]
         L.dreamer_route_counts.argtypes = [vp, vp, i, vp]
         L.dreamer_route_experts.argtypes = [vp, i, vp, i, vp, vp, vp, vp]
         L.dreamer_bias_update.argtypes = [vp, C.c_float, vp, vp]
@@ -86,6 +93,7 @@ def lib(path: str = LIB_PATH):
         L.dreamer_strerror.argtypes = [i]
         L.dreamer_strerror.restype = C.c_char_p
         for f in ("dreamer_init", "dreamer_core_forward", "dreamer_decode_step",
+                  "dreamer_core_forward_packed", "dreamer_decode_step_kv4",
                   "dreamer_route_counts", "dreamer_route_experts", "dreamer_bias_update",
                   "dreamer_bias_update_counts", "dreamer_route_balance",
                   "dreamer_set_profiling", "dreamer_get_stats"):
@@ -187,6 +195,42 @@ class Dreamer:
                                          _ptr(cache_len), _ptr(x_out),
                                          C.byref(tr) if tr is not None else None,
                                          _stream(stream)), "dreamer_decode_step")
+        return x_out
+
+    def forward_packed(self, x_in, cu_seqlens, x_out=None, depth_begin=0, depth_end=None,
+                       da_kv=None, trace: dict | None = None, stream=None):
+        """The forward over packed prompts of any lengths: x_in [tokens][hidden], cu_seqlens a CUDA
+        int32 tensor [prompts + 1] from 0 to the number of tokens.  The trace's sa_k and sa_v are
+        the rows that KV4Cache.store takes."""
+        cfg = self.cfg
+        depth_end = cfg.depth if depth_end is None else depth_end
+        if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or cu_seqlens.dim() != 1 or \
+                not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens: a contiguous CUDA int32 tensor [prompts + 1]")
+        if x_out is None:
+            x_out = torch.empty_like(x_in)
+        tr = self._trace(trace)
+        _check(self.L.dreamer_core_forward_packed(
+            self.h, _ptr(x_in), _ptr(x_out), _ptr(cu_seqlens), int(cu_seqlens.shape[0]) - 1,
+            int(x_in.shape[0]), int(depth_begin), int(depth_end), _ptr(da_kv),
+            C.byref(tr) if tr is not None else None, _stream(stream)), "dreamer_core_forward_packed")
+        return x_out
+
+    def decode_step_kv4(self, x_new, cache, cache_len, x_out=None, trace: dict | None = None,
+                        stream=None):
+        """One decode step over a 4-bit cache (attention.KV4Cache with the handle's depth, batch
+        and heads, a capacity of at least max_cache_len): the new tokens' keys and values are
+        quantised into position cache_len[b] of every depth, and cache_len[b] + 1 are attended."""
+        if cache.depth != self.cfg.depth:
+            raise ValueError(f"cache: {self.cfg.depth} depths, not {cache.depth}")
+        if x_out is None:
+            x_out = torch.empty_like(x_new)
+        tr = self._trace(trace)
+        cc = KV4CacheC(cache.data.data_ptr(), cache.batch, cache.n_kv_heads, cache.head_dim,
+                       cache.capacity)
+        _check(self.L.dreamer_decode_step_kv4(self.h, _ptr(x_new), C.byref(cc), _ptr(cache_len),
+                                             _ptr(x_out), C.byref(tr) if tr is not None else None,
+                                             _stream(stream)), "dreamer_decode_step_kv4")
         return x_out
 
     def route_balance(self, depth: int = -1, stream=None):

@@ -288,6 +288,27 @@ int dreamer_attn_kv4(const dreamer_kv4_cache *cache, const void *q, int64_t ldq,
                      int64_t ldo, const int32_t *lens, int n_heads, int dtype, float scale,
                      int32_t *status, dreamer_stream stream);
 
+/* dreamer_core_forward over packed prompts of different lengths: n_seq prompts with tokens
+ * cu_seqlens[i] .. cu_seqlens[i+1]-1 (int32 [n_seq+1], device; cu_seqlens[0] = 0, not decreasing,
+ * cu_seqlens[n_seq] = n_tokens), each with its own positions 0, 1, ... and its own causal sequence
+ * attention.  1 <= n_tokens <= batch*seq (or batch for a decode-only handle); prompts of at most
+ * max(seq, max_cache_len) + 1 tokens, of any length: a bfloat16 handle's seq needs to be no multiple
+ * of 128 for this call.  x_in, x_out, da_kv and the trace are as in dreamer_core_forward with
+ * T = n_tokens; the traced sa_k / sa_v rows are what dreamer_kv4_store takes.  Boundaries that are
+ * not as above are reported by the next call (DREAMER_ERR_ARG).                             */
+int dreamer_core_forward_packed(dreamer_handle *h, const void *x_in, void *x_out,
+                                const int32_t *cu_seqlens, int n_seq, int n_tokens,
+                                int depth_begin, int depth_end, void *da_kv,
+                                const dreamer_trace *trace, dreamer_stream stream);
+
+/* dreamer_decode_step over 4-bit caches: cache->data holds the depths' caches one behind the
+ * other ([L] of dreamer_kv4_bytes() each), batch, n_kv_heads = n_heads and head_dim those of the
+ * handle, capacity at least max_cache_len.  Each depth quantises the new token's key and value
+ * into position cache_len[b] (< max_cache_len) and attends cache_len[b] + 1 positions.       */
+int dreamer_decode_step_kv4(dreamer_handle *h, const void *x_new, const dreamer_kv4_cache *cache,
+                            const int32_t *cache_len, void *x_out, const dreamer_trace *trace,
+                            dreamer_stream stream);
+
 /* Instrumentation.  Stages of the depth step, in launch order: */
 enum {
   DREAMER_STAGE_NORM = 0,     /* RMSNorm of the residual stream                          */
