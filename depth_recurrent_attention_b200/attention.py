@@ -9,6 +9,7 @@ asynchronous on `stream` (default: the current stream of the tensors' device).
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 
 import torch
@@ -33,12 +34,21 @@ def _lib():
         rows = [vp, vp, i64, vp, i64, vp, vp, i, i, vp, vp]
         L.dreamer_kv4_store.argtypes = rows
         L.dreamer_kv4_load.argtypes = rows[:9] + [i, vp, vp]
-        L.dreamer_attn_kv4.argtypes = [vp, vp, i64, vp, i64, vp, i, i, f, vp, vp]
+        L.dreamer_attn_kv4.argtypes = [vp, vp, i64, vp, i64, vp, i, i, f, vp, i64, vp, vp]
+        L.dreamer_attn_kv4_workspace.argtypes = [vp, i]
+        L.dreamer_attn_kv4_workspace.restype = i64
         L.dreamer_attn_packed.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i, i, i, i, i, i, f, vp, vp]
         for n in ("dreamer_kv4_store", "dreamer_kv4_load", "dreamer_attn_kv4", "dreamer_attn_packed"):
             getattr(L, n).restype = i
         _fns = L
     return _fns
+
+
+try:  # the current stream's handle without a Stream object
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _rows(name, t, device, heads=None, dim=None, dtype=None, n=None):
@@ -52,17 +62,17 @@ def _rows(name, t, device, heads=None, dim=None, dtype=None, n=None):
         raise ValueError(f"{name}: {tuple(t.shape)} of {t.dtype} does not fit the other arguments")
     ld, sh, sd = t.stride()
     if r <= 1:
-        ld = max(h * d, -(-h * d // 8) * 8)
+        ld = -(-h * d // 8) * 8
     if (sd != 1 and d > 1) or (sh != d and h > 1) or ld < h * d:
         raise ValueError(f"{name}: a row's heads have to lie densely (strides {t.stride()})")
-    if r and (t.data_ptr() % 16 or (ld * t.element_size()) % 16):
+    if r and (t.data_ptr() % 16 or ld * t.element_size() % 16):
         raise ValueError(f"{name}: rows have to be 16-byte aligned")
     return ld
 
 
 def _ints(name, t, device, n):
     if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int32 or \
-            t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+            t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 tensor of {n} on {device}")
     return t.data_ptr()
 
@@ -76,23 +86,40 @@ def _status(t, device):
 
 
 def _scale(scale, dim):
-    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    scale = dim ** -0.5 if scale is None else float(scale)
     if not math.isfinite(scale):
         raise ValueError("scale: a finite number")
     return scale
 
 
+def _empty(shape, dtype, device, stream):
+    """New memory that belongs to the stream it is used on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(fn, what, device, stream, *args):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = _raw_stream(device.index)
     elif stream.device != device:
         raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
+    else:
+        handle = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream), what)
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream), what)
-    return stream
+            rc = fn(*args, handle)
+    _check(rc, what)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace(batch, kv_heads, dim, capacity, heads, index):
+    with torch.cuda.device(index):
+        return _lib().dreamer_attn_kv4_workspace(
+            C.byref(KV4CacheC(None, batch, kv_heads, dim, capacity)), heads)
 
 
 def attn_packed(q, k, v, cu_seqlens, out=None, scale=None, status=None, stream=None):
@@ -113,19 +140,19 @@ def attn_packed(q, k, v, cu_seqlens, out=None, scale=None, status=None, stream=N
     ldv = _rows("v", v, dev, hk, d, q.dtype, n)
     if hk < 1 or hq < 1 or hq % hk:
         raise ValueError(f"{hq} query heads over {hk} key heads")
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+    prompts = cu_seqlens.numel() - 1 if isinstance(cu_seqlens, torch.Tensor) else -1
+    if prompts < 0:
         raise ValueError("cu_seqlens: int32 [prompts + 1]")
-    cu = _ints("cu_seqlens", cu_seqlens, dev, cu_seqlens.shape[0])
+    cu = _ints("cu_seqlens", cu_seqlens, dev, prompts + 1)
     if out is None:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-            out = torch.empty((n, hq, d), dtype=q.dtype, device=dev)
+        out = _empty((n, hq, d), q.dtype, dev, stream)
     ldo = _rows("out", out, dev, hq, d, q.dtype, n)
     scale = _scale(scale, d)
     if not scale > 0:
         raise ValueError("scale: positive")
     if n:
         _call(_lib().dreamer_attn_packed, "dreamer_attn_packed", dev, stream, q.data_ptr(), ldq,
-              k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, cu, cu_seqlens.shape[0] - 1,
+              k.data_ptr(), ldk, v.data_ptr(), ldv, out.data_ptr(), ldo, cu, prompts,
               n, hq, hk, d, _DTYPES[q.dtype], scale, _status(status, dev))
     return out
 
@@ -149,7 +176,6 @@ class KV4Cache:
         self.capacity = blocks * BLOCK
         self.device = data.device
         self._step = data.stride(0)
-        self._c = KV4CacheC(None, self.batch, self.n_kv_heads, head_dim, self.capacity)
         self._base = data.data_ptr()
 
     @staticmethod
@@ -197,8 +223,7 @@ class KV4Cache:
         fresh = out is None
         if fresh:
             shape = (n_rows, self.n_kv_heads, self.head_dim)
-            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-                out = (torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev))
+            out = _empty(shape, dtype, dev, stream), _empty(shape, dtype, dev, stream)
         k, v = out
         ldk = _rows("out[0]", k, dev, self.n_kv_heads, self.head_dim, dtype, n_rows)
         ldv = _rows("out[1]", v, dev, self.n_kv_heads, self.head_dim, dtype, n_rows)
@@ -220,10 +245,12 @@ class KV4Cache:
         if hq < 1 or hq % self.n_kv_heads:
             raise ValueError(f"q: a multiple of {self.n_kv_heads} heads")
         if out is None:
-            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-                out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            out = _empty(q.shape, q.dtype, dev, stream)
         ldo = _rows("out", out, dev, hq, self.head_dim, q.dtype, self.batch)
+        need = _workspace(self.batch, self.n_kv_heads, self.head_dim, self.capacity, hq, dev.index)
+        ws = _empty((need,), torch.uint8, dev, stream) if need else None
         _call(_lib().dreamer_attn_kv4, "dreamer_attn_kv4", dev, stream, C.byref(self._at(depth)),
               q.data_ptr(), ldq, out.data_ptr(), ldo, _ints("lens", lens, dev, self.batch), hq,
-              _DTYPES[q.dtype], _scale(scale, self.head_dim), _status(status, dev))
+              _DTYPES[q.dtype], _scale(scale, self.head_dim), ws.data_ptr() if need else None, need,
+              _status(status, dev))
         return out

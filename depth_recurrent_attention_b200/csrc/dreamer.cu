@@ -51,6 +51,7 @@ struct dreamer_handle {
   void *Ybuf = nullptr;          // [T k + 128][h] expert outputs in sorted order
   int *pcnt = nullptr, *poffs = nullptr, *ptiles_a = nullptr, *ptiles_b = nullptr;
   int *pcursor = nullptr, *prows = nullptr, *pinv = nullptr;
+  void *kv4_ws = nullptr;        // workspace of attention over 4-bit caches
   int *pos = nullptr;            // [T] positions of packed prompts' tokens
   int *err = nullptr;
   void *k3 = nullptr;            // [E][3 d_r] bf16: router keys repeated for split scores
@@ -490,6 +491,8 @@ extern "C" int dreamer_init(const dreamer_config *cfg, const dreamer_weights *w,
       if (ns > by_len) ns = by_len;
       h->nsplit = (int)(ns < 1 ? 1 : ns > 64 ? 64 : ns);
       DALLOC(h->part, (size_t)c.batch * c.n_heads * h->nsplit * (d + 2) * sizeof(float));
+      if (d == 64 || d == 128)
+        DALLOC(h->kv4_ws, ops::kv4_attn_workspace(ops::Kv4Cache{nullptr, c.batch, c.n_heads, d, 0}, c.n_heads, true));
     }
     CK(cudaMemset(h->err, 0, sizeof(int)));
     CK(cudaMemset(h->counts, 0, (size_t)L * E * sizeof(int)));
@@ -1011,13 +1014,13 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
       ops::Kv4Attn a4{};
       a4.q = h->qkv_sa; a4.ldq = 3 * hd; a4.out = h->attn; a4.ldo = 2 * hd;
       a4.lens = io.cache_len; a4.len_add = 1; a4.Hq = c.n_heads; a4.dtype = c.dtype;
-      a4.scale = 1.0f / sqrtf((float)d); a4.err = h->err;
+      a4.scale = 1.0f / sqrtf((float)d); a4.workspace = h->kv4_ws; a4.err = h->err;
       ops::LaunchOpt o;
       o.pdl = pdl_take(h, st);
       if (ops::kv4_store(c4, r4, st, o) != DREAMER_OK) h->path_err = 1;
       o.pdl = pdl_take(h, st);
       if (ops::kv4_attn(c4, a4, st, o) != DREAMER_OK) h->path_err = 1;
-      g_launches += 2;
+      g_launches += ops::kv4_attn_workspace(c4, c.n_heads) ? 3 : 2;
       return;
     }
     if (io.mode == 3) {

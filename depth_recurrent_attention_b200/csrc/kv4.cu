@@ -204,22 +204,26 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
 }
 
 // ---- attention of one query token a sequence over the cache ------------------------------
-// One warp takes whole 64-token blocks, brought in by bulk copies into a ring of its own.
-// Products run on warp-level matrix instructions (m16n8k16) with the codes as the A operand:
-//   scores   A = 16 keys x 16 channels of K codes, B = channels x 8 columns of q
+// A warp takes whole 64-token blocks, brought in by bulk copies into a ring of its own, and
+// multiplies on warp-level matrix instructions with the codes as the A operand:
+//   scores   A = 16 keys x channels of K codes, B = channels x 8 columns of q
 //   output   A = 16 channels x 16 keys of V codes, B = keys x 8 columns of weights
-// A code c enters as the bf16 number c - 8, exact: (0x4300 | c) is 128 + c.  With
-// value = s (c - 8) + (m + 8 s), a score is s (q . (c - 8)) + (m + 8 s) sum(q), and a weight p
-// enters the output product as p s, the offsets as one sum of p (m + 8 s) a plane.
-// A column is (16-key tile of the supertile, query head): GP = 2, 4 or 8 columns hold the query
-// heads that share a key head, and 8 / GP key tiles share one accumulator, each with q in its own
-// columns and zeros elsewhere.  So one exponential a (key, query head) is computed also where a
-// key head has one query head (GP = 2: one idle column of two).  Every column keeps its own
-// running maximum and sum; they join at the end: lanes, then warps in shared memory, then the
-// CTAs of a cluster (one (sequence, key head) split over the key axis) in distributed shared
-// memory.  No workspace, no atomics: the same inputs give the same bits.
+// What bounds it is turning nibbles into operands (the integer pipe), so
+//   - bfloat16 scores run on 8-bit integer products (m16n8k32): a mask and a shift make four
+//     codes a word, and q enters as a 16-bit fixed-point number of its plane's largest |q|, in two
+//     signed bytes; the integer sums are exact, a score is off by about 2^-16 of the largest product,
+//     far below the bf16 rounding of the weights;
+//   - float32 scores, and the output products, take a code as the bf16 number c - 8, exact:
+//     (0x4300 | c) is 128 + c; float32 operands enter in three bf16 terms.
+// With value = s c + m a score is s (q . c) + m sum(q); a weight p enters the output product as p s,
+// the offsets as one sum of p (m + 8 s) a plane.
+// A column is (16-key tile of a supertile, query head): GP = 2, 4 or 8 columns hold the query heads
+// that share a key head, and 8 / GP key tiles share one accumulator, each with q in its own columns
+// and zeros elsewhere.  So one exponential a (key, query head) is computed also where a key head has
+// one query head (GP = 2: one idle column of two).  Every column keeps its own running maximum and
+// sum; they join at the end of a (sequence, key head): lanes, then warps.
 //
-// The rows r of a 16-key tile are the keys perm(r): with it a warp's 8-byte reads of K rows and
+// The rows r of a 16-key tile are the keys perm_row(r): with it a warp's 8-byte reads of K rows and
 // 4-byte reads of V rows meet every bank once.
 struct AttnArgs {
   const uint8_t *data;
@@ -232,6 +236,8 @@ struct AttnArgs {
   int len_add;
   float scale_log2;
   int *err;
+  float *part;   // split form: [slot][GP][D + 4] partial outputs, maximum, sum
+  int n_warps;   // split form: warps of the grid
 };
 
 __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
@@ -239,6 +245,14 @@ __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// unsigned bytes times signed bytes, 32-bit integer sums
+__device__ __forceinline__ void mma16832(int *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // transpose of an 8 x 8 matrix of 16-bit values held as mma fragments
@@ -255,205 +269,197 @@ template <int J> __device__ __forceinline__ uint32_t codes2(uint32_t w) {
   return r;
 }
 __device__ __forceinline__ int perm_row(int g) { return (g & 1) ? 4 + ((g >> 1) ^ 2) : g >> 1; }
+__device__ __forceinline__ float2 pair_at(const uint8_t *p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 
-template <int NG, int GP, int TERMS, int NW, int ST>
-struct AttnCfg {
-  static constexpr int BLK = NG * 2 * (PLANE + PAIRS);  // bytes of a block
-  static constexpr int RING = NW * ST * BLK;
+// An integer sum below 2^22 in magnitude, started at MAGIC, read as a float is 1.5 * 2^23 + sum.
+constexpr int MAGIC = 0x4B400000;
+constexpr float MAGIC_F = 12582912.f;
+
+// The attention of one warp over blocks of one (sequence, key head) for up to GP query heads.
+template <typename T, int NG, int GP>
+struct WarpAttn {
+  static constexpr bool INT = sizeof(T) == 2;       // scores on integer products
+  static constexpr int TERMS = sizeof(T) == 2 ? 1 : 3;  // bf16 terms of a weight (and of a float32 q)
   static constexpr int D = NG * 64;
-  // after the loop the ring holds [NW][GP][D] partial outputs
-  static constexpr int SMEM = RING > NW * GP * D * 4 ? RING : NW * GP * D * 4;
-};
+  static constexpr int NTI = 8 / GP;                // key tiles that share an accumulator
+  static constexpr int NSUP = 4 / NTI;              // accumulators of a block
+  static constexpr int QR = INT ? 8 : 24;           // registers of q a plane
+  static constexpr int BLK = NG * 2 * (PLANE + PAIRS);  // bytes of a block
 
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-}
+  uint32_t qf[NG][QR];
+  float qs[NG][2];     // sum(q) of this lane's columns 2t, 2t + 1, times scale_log2
+  float qi[NG][2];     // INT: the columns' fixed-point step, times scale_log2
+  float o[NG][4][4];   // [plane][channel tile][c]: channels 8g + mt, 8g + 4 + mt, columns 2t, 2t + 1
+  float ofs[NG][2];    // sum of p (m + 8 s)
+  float m2[2], l2[2];
 
-template <typename T, int NG, int GP, int TERMS, int NW, int ST>
-__global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
-  using C = AttnCfg<NG, GP, TERMS, NW, ST>;
-  constexpr int D = C::D;
-  constexpr int NTI = 8 / GP;       // key tiles that share an accumulator
-  constexpr int NSUP = 4 / NTI;     // accumulators of a block
-  extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(8) uint64_t bars[NW * ST];
-  __shared__ float sm_m[NW][GP], sm_l[NW][GP];       // of a warp's columns, joined over its tiles
-  __shared__ float so[GP][D], sM[GP], sL[GP];        // of the CTA
-  __shared__ int s_abort;
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  uint32_t crank, csize;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
-  const int item = blockIdx.x / csize;
-  const int qc = item % a.qchunks, pair = item / a.qchunks;
-  const int b = pair / a.Hkv, kvh = pair % a.Hkv;
-  const int nq = min(GP, a.G - qc * GP);             // query heads of this CTA
-  const int head0 = kvh * a.G + qc * GP;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NW * ST; i++) tc::mbar_init(tc::smem_u32(&bars[i]), 1);
-    tc::fence_mbar_init();
-    s_abort = 0;
-  }
-  __syncthreads();
-
-  long len = (long)a.lens[b] + a.len_add;
-  if (len < 0 || len > a.cap) {                      // reported, and attends to nothing
-    if (threadIdx.x == 0) raise_dev_error(a.err, DEV_BAD_INDEX);
-    len = 0;
-  }
-  const int nkeys = (int)len;
-  const int nb = (nkeys + KV4_BLOCK - 1) / KV4_BLOCK;
-  const int per = (nb + (int)csize - 1) / (int)csize;
-  const int blk0 = min(nb, (int)crank * per), blk1 = min(nb, blk0 + per);
-  const uint8_t *base = a.data + (long)pair * (a.cap / KV4_BLOCK) * C::BLK;
-  const int mine = blk1 - blk0 > warp ? (blk1 - blk0 - warp + NW - 1) / NW : 0;
-  uint8_t *wring = ring + warp * ST * C::BLK;
-  auto issue = [&](int i) {  // block i of this warp
-    const uint32_t bar = tc::smem_u32(&bars[warp * ST + i % ST]);
-    tc::mbar_expect_tx(bar, C::BLK);
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            tc::smem_u32(wring + (i % ST) * C::BLK)),
-        "l"(base + (long)(blk0 + warp + i * NW) * C::BLK), "r"((uint32_t)C::BLK), "r"(bar)
-        : "memory");
-  };
-  if (lane == 0)
-    for (int i = 0; i < ST && i < mine; i++) issue(i);
-
-  // q as B fragments (column g: query head g % GP; channels 16 t .. 16 t + 15 of a plane), in
-  // TERMS bf16 terms that add up to q, and sum(q) of a plane for this lane's columns 2t, 2t + 1
-  uint32_t qf[NG][8][TERMS];
-  float qs[NG][2];
-  {
+  // q as B fragments: column g is query head g % GP; a lane holds channels 16 t .. 16 t + 15 of a plane
+  __device__ __forceinline__ void start(const T *q, int nq, float scale_log2) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int qh = g % GP;
-    const T *qp = reinterpret_cast<const T *>(a.q) + (long)b * a.ldq + (long)(head0 + (qh < nq ? qh : 0)) * D + 16 * t;
+    const T *qp = q + (long)(qh < nq ? qh : 0) * D + 16 * t;
 #pragma unroll
     for (int p = 0; p < NG; p++) {
       float v[16];
       load8(qp + p * 64, v);
       load8(qp + p * 64 + 8, v + 8);
-      float sum = 0.f;
+      float sum = 0.f, amax = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; e++) {
         if (qh >= nq) v[e] = 0.f;
         sum += v[e];
+        amax = fmaxf(amax, fabsf(v[e]));
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      qs[p][0] = __shfl_sync(0xffffffffu, sum, ((2 * t) % GP) * 4) * a.scale_log2;
-      qs[p][1] = __shfl_sync(0xffffffffu, sum, ((2 * t + 1) % GP) * 4) * a.scale_log2;
+      const int c0 = ((2 * t) % GP) * 4, c1 = ((2 * t + 1) % GP) * 4;
+      qs[p][0] = __shfl_sync(0xffffffffu, sum, c0) * scale_log2;
+      qs[p][1] = __shfl_sync(0xffffffffu, sum, c1) * scale_log2;
+      if constexpr (INT) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 127 * 256 steps to the largest |q|; a q that is not finite leaves sum(q) so, and its
+        // scores with it.  The step is kept a normal number (values that small add nothing).
+        const bool ok = amax >= 0x1p-110f && amax <= 0x1.fffffep127f;
+        const float step = ok ? amax / 32512.f : 1.f, inv = ok ? 32512.f / amax : 0.f;
+        qi[p][0] = __shfl_sync(0xffffffffu, step, c0) * scale_log2;
+        qi[p][1] = __shfl_sync(0xffffffffu, step, c1) * scale_log2;
 #pragma unroll
-      for (int w = 0; w < 2; w++)
+        for (int w = 0; w < 4; w++) {  // even channels of the low 8, odd ones, then of the high 8
+          uint32_t hi = 0, lo = 0;
 #pragma unroll
-        for (int j = 0; j < 4; j++) {  // the order of codes2<j> of word w: elements j and j + 4
-          float lo = v[8 * w + j], hi = v[8 * w + j + 4];
+          for (int e = 0; e < 4; e++) {
+            const int x = ok ? __float2int_rn(v[(w >> 1) * 8 + 2 * e + (w & 1)] * inv) : 0;
+            const int h = (x + 128) >> 8;
+            hi |= (uint32_t)(h & 255) << (8 * e);
+            lo |= (uint32_t)((x - h * 256) & 255) << (8 * e);
+          }
+          qf[p][2 * w] = hi;
+          qf[p][2 * w + 1] = lo;
+        }
+      } else {
+        qi[p][0] = qi[p][1] = scale_log2;
 #pragma unroll
-          for (int k = 0; k < TERMS; k++) {
-            const uint32_t pk = bf2_pack_rn(lo, hi);
-            qf[p][4 * w + j][k] = pk;
-            lo -= __uint_as_float(pk << 16);
-            hi -= __uint_as_float(pk & 0xffff0000u);
+        for (int w = 0; w < 2; w++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {  // the order of codes2<j> of word w: elements j and j + 4
+            float lo = v[8 * w + j], hi = v[8 * w + j + 4];
+#pragma unroll
+            for (int k = 0; k < 3; k++) {
+              const uint32_t pk = bf2_pack_rn(lo, hi);
+              qf[p][(4 * w + j) * 3 + k] = pk;
+              lo -= __uint_as_float(pk << 16);
+              hi -= __uint_as_float(pk & 0xffff0000u);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+      m2[c] = -INFINITY;
+      l2[c] = 0.f;
+    }
+#pragma unroll
+    for (int p = 0; p < NG; p++) {
+      ofs[p][0] = ofs[p][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < 4; mt++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) o[p][mt][c] = 0.f;
+    }
+  }
+
+  // q . c (integer form: c; float form: c - 8) of supertile sp in plane p for this lane's two keys and
+  // columns, to be scaled by qi and s
+  __device__ __forceinline__ void products(const uint8_t *blk, int sp, int p, float *f) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint8_t *kr = blk + p * PLANE + (sp * NTI * 16 + perm_row(g)) * 32 + 8 * t;
+    if constexpr (INT) {
+      int hi[4] = {MAGIC, MAGIC, MAGIC, MAGIC}, lo[4] = {MAGIC, MAGIC, MAGIC, MAGIC};
+#pragma unroll
+      for (int ti = 0; ti < NTI; ti++) {
+        const uint2 w0 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32);
+        const uint2 w1 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32 + 8 * 32);
+        const bool on = GP == 8 || g / GP == ti;
+        const uint32_t ww0[2] = {w0.x, w0.y}, ww1[2] = {w1.x, w1.y};
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+          const uint32_t a[4] = {ww0[w] & 0x0f0f0f0fu, ww1[w] & 0x0f0f0f0fu, (ww0[w] >> 4) & 0x0f0f0f0fu,
+                                 (ww1[w] >> 4) & 0x0f0f0f0fu};
+          mma16832(hi, a, on ? qf[p][4 * w] : 0u, on ? qf[p][4 * w + 2] : 0u);
+          mma16832(lo, a, on ? qf[p][4 * w + 1] : 0u, on ? qf[p][4 * w + 3] : 0u);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; c++)
+        f[c] = fmaf(256.f, __int_as_float(hi[c]) - MAGIC_F, __int_as_float(lo[c]) - MAGIC_F);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; c++) f[c] = 0.f;
+#pragma unroll
+      for (int ti = 0; ti < NTI; ti++) {
+        const uint2 w0 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32);
+        const uint2 w1 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32 + 8 * 32);
+        const bool on = GP == 8 || g / GP == ti;
+        const uint32_t ww0[2] = {w0.x, w0.y}, ww1[2] = {w1.x, w1.y};
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+          const uint32_t f0[4] = {codes2<0>(ww0[w]), codes2<0>(ww1[w]), codes2<1>(ww0[w]), codes2<1>(ww1[w])};
+          const uint32_t f1[4] = {codes2<2>(ww0[w]), codes2<2>(ww1[w]), codes2<3>(ww0[w]), codes2<3>(ww1[w])};
+#pragma unroll
+          for (int k = 2; k >= 0; k--) {
+            mma16816(f, f0, on ? qf[p][12 * w + k] : 0u, on ? qf[p][12 * w + 3 + k] : 0u);
+            mma16816(f, f1, on ? qf[p][12 * w + 6 + k] : 0u, on ? qf[p][12 * w + 9 + k] : 0u);
           }
         }
+      }
     }
   }
 
-  float o[NG][4][4];   // [plane][channel tile][c]: channels 8g + mt and 8g + 4 + mt, columns 2t, 2t + 1
-  float ofs[NG][2];    // sum of p (m + 8 s)
-  float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
-#pragma unroll
-  for (int p = 0; p < NG; p++) {
-    ofs[p][0] = ofs[p][1] = 0.f;
-#pragma unroll
-    for (int mt = 0; mt < 4; mt++)
-#pragma unroll
-      for (int c = 0; c < 4; c++) o[p][mt][c] = 0.f;
-  }
-  const int prow = perm_row(g);                       // key of row g of a tile
-  const int pv0 = perm_row(2 * t), pv1 = perm_row(2 * t + 1);
-  const int my_tile = (2 * t) / GP;                   // tile of this lane's columns
-  bool ok = true;
-  int done = 0;
-
-  for (int i = 0; i < mine; i++) {
-    if (!tc::mbar_wait(tc::smem_u32(&bars[warp * ST + i % ST]), (uint32_t)((i / ST) & 1), (volatile int *)&s_abort, a.err)) {
-      ok = false;
-      break;
-    }
-    done = i + 1;
-    const uint8_t *blk = wring + (i % ST) * C::BLK;
-    const int key0 = (blk0 + warp + i * NW) * KV4_BLOCK;
+  // One block in shared memory: keys key0 .. key0 + 63, of which those below nkeys exist
+  __device__ __forceinline__ void block(const uint8_t *blk, int key0, int nkeys) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int my_key = ((2 * t) / GP) * 16 + perm_row(g);  // in a supertile: this lane's keys my_key (+ 8)
     const bool tail = key0 + KV4_BLOCK > nkeys;
-    // ---- scores
     float x[NSUP][4];
 #pragma unroll
     for (int sp = 0; sp < NSUP; sp++) {
 #pragma unroll
-      for (int c = 0; c < 4; c++) x[sp][c] = 0.f;
-#pragma unroll
       for (int p = 0; p < NG; p++) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ti = 0; ti < NTI; ti++) {
-          const uint8_t *kr = blk + p * PLANE + ((sp * NTI + ti) * 16 + prow) * 32 + 8 * t;
-          const uint2 w0 = *reinterpret_cast<const uint2 *>(kr);
-          const uint2 w1 = *reinterpret_cast<const uint2 *>(kr + 8 * 32);
-          const bool on = GP == 8 || g / GP == ti;
-          const uint32_t ww0[2] = {w0.x, w0.y}, ww1[2] = {w1.x, w1.y};
-#pragma unroll
-          for (int w = 0; w < 2; w++) {
-            uint32_t f0[4] = {codes2<0>(ww0[w]), codes2<0>(ww1[w]), codes2<1>(ww0[w]), codes2<1>(ww1[w])};
-            uint32_t f1[4] = {codes2<2>(ww0[w]), codes2<2>(ww1[w]), codes2<3>(ww0[w]), codes2<3>(ww1[w])};
-#pragma unroll
-            for (int k = TERMS - 1; k >= 0; k--) {
-              mma16816(acc, f0, on ? qf[p][4 * w][k] : 0u, on ? qf[p][4 * w + 1][k] : 0u);
-              mma16816(acc, f1, on ? qf[p][4 * w + 2][k] : 0u, on ? qf[p][4 * w + 3][k] : 0u);
-            }
-          }
-        }
-        const uint8_t *kp = blk + 2 * NG * PLANE + p * PAIRS + ((sp * NTI + my_tile) * 16 + prow) * 4;
-        const float2 s0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(kp));
-        const float2 s1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(kp + 8 * 4));
-        const float u0 = s0.x * a.scale_log2, u1 = s1.x * a.scale_log2;
-        const float z0 = fmaf(8.f, s0.x, s0.y), z1 = fmaf(8.f, s1.x, s1.y);
-        x[sp][0] += fmaf(u0, acc[0], z0 * qs[p][0]);
-        x[sp][1] += fmaf(u0, acc[1], z0 * qs[p][1]);
-        x[sp][2] += fmaf(u1, acc[2], z1 * qs[p][0]);
-        x[sp][3] += fmaf(u1, acc[3], z1 * qs[p][1]);
+        float f[4];
+        products(blk, sp, p, f);
+        const uint8_t *kp = blk + 2 * NG * PLANE + p * PAIRS + (sp * NTI * 16 + my_key) * 4;
+        const float2 s0 = pair_at(kp), s1 = pair_at(kp + 8 * 4);
+        const float z0 = INT ? s0.y : fmaf(8.f, s0.x, s0.y), z1 = INT ? s1.y : fmaf(8.f, s1.x, s1.y);
+        const float y0 = fmaf(s0.x * qi[p][0], f[0], z0 * qs[p][0]), y1 = fmaf(s0.x * qi[p][1], f[1], z0 * qs[p][1]);
+        const float y2 = fmaf(s1.x * qi[p][0], f[2], z1 * qs[p][0]), y3 = fmaf(s1.x * qi[p][1], f[3], z1 * qs[p][1]);
+        x[sp][0] = p == 0 ? y0 : x[sp][0] + y0;
+        x[sp][1] = p == 0 ? y1 : x[sp][1] + y1;
+        x[sp][2] = p == 0 ? y2 : x[sp][2] + y2;
+        x[sp][3] = p == 0 ? y3 : x[sp][3] + y3;
       }
       if (tail) {
-        const int key = key0 + (sp * NTI + my_tile) * 16 + prow;
+        const int key = key0 + sp * NTI * 16 + my_key;
         if (key >= nkeys) x[sp][0] = x[sp][1] = -INFINITY;
         if (key + 8 >= nkeys) x[sp][2] = x[sp][3] = -INFINITY;
       }
     }
-    // ---- running maximum of the two columns, moved only when it grows by more than 2^8
+    // running maximum of the two columns, moved only when some score passes it by more than 2^8
     float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
 #pragma unroll
     for (int sp = 1; sp < NSUP; sp++) {
       mx0 = fmaxf(mx0, fmaxf(x[sp][0], x[sp][2]));
       mx1 = fmaxf(mx1, fmaxf(x[sp][1], x[sp][3]));
     }
-#pragma unroll
-    for (int k = 4; k < 32; k <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, k));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, k));
-    }
     if (__any_sync(0xffffffffu, mx0 > m2[0] + 8.f || mx1 > m2[1] + 8.f)) {
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, k));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, k));
+      }
       const float n0 = fmaxf(m2[0], mx0), n1 = fmaxf(m2[1], mx1);
       const float a0 = m2[0] == -INFINITY ? 0.f : tc::ex2(m2[0] - n0);
       const float a1 = m2[1] == -INFINITY ? 0.f : tc::ex2(m2[1] - n1);
@@ -475,7 +481,6 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
       }
     }
     const float r0 = m2[0] == -INFINITY ? 0.f : m2[0], r1 = m2[1] == -INFINITY ? 0.f : m2[1];
-    // ---- weights and output
     float ob[NG][4][4];  // TERMS > 1: the block's own sums, added in 32-bit rounding to nearest
     if (TERMS > 1) {
 #pragma unroll
@@ -485,6 +490,7 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
           for (int c = 0; c < 4; c++) ob[p][mt][c] = 0.f;
     }
+    const int pv0 = perm_row(2 * t) * 32 + 4 * g, pv1 = perm_row(2 * t + 1) * 32 + 4 * g;
 #pragma unroll
     for (int sp = 0; sp < NSUP; sp++) {
       const float p0 = tc::ex2(x[sp][0] - r0), p1 = tc::ex2(x[sp][1] - r1);
@@ -493,11 +499,10 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
       l2[1] += p1 + p3;
 #pragma unroll
       for (int p = 0; p < NG; p++) {
-        const uint8_t *vp = blk + 2 * NG * PLANE + (NG + p) * PAIRS + ((sp * NTI + my_tile) * 16 + prow) * 4;
-        float2 s0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(vp));
-        float2 s1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(vp + 8 * 4));
+        const uint8_t *vp = blk + 2 * NG * PLANE + (NG + p) * PAIRS + (sp * NTI * 16 + my_key) * 4;
+        float2 s0 = pair_at(vp), s1 = pair_at(vp + 8 * 4);
         if (tail) {  // what lies behind the last key may be anything
-          const int key = key0 + (sp * NTI + my_tile) * 16 + prow;
+          const int key = key0 + sp * NTI * 16 + my_key;
           if (key >= nkeys) s0 = make_float2(0.f, 0.f);
           if (key + 8 >= nkeys) s1 = make_float2(0.f, 0.f);
         }
@@ -520,11 +525,11 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
         }
 #pragma unroll
         for (int ti = 0; ti < NTI; ti++) {
-          const uint8_t *vr = blk + (NG + p) * PLANE + (sp * NTI + ti) * 16 * 32 + 4 * g;
-          const uint32_t v0 = *reinterpret_cast<const uint32_t *>(vr + pv0 * 32);
-          const uint32_t v1 = *reinterpret_cast<const uint32_t *>(vr + pv1 * 32);
-          const uint32_t v2 = *reinterpret_cast<const uint32_t *>(vr + (pv0 + 8) * 32);
-          const uint32_t v3 = *reinterpret_cast<const uint32_t *>(vr + (pv1 + 8) * 32);
+          const uint8_t *vr = blk + (NG + p) * PLANE + (sp * NTI + ti) * 16 * 32;
+          const uint32_t v0 = *reinterpret_cast<const uint32_t *>(vr + pv0);
+          const uint32_t v1 = *reinterpret_cast<const uint32_t *>(vr + pv1);
+          const uint32_t v2 = *reinterpret_cast<const uint32_t *>(vr + pv0 + 8 * 32);
+          const uint32_t v3 = *reinterpret_cast<const uint32_t *>(vr + pv1 + 8 * 32);
           const uint32_t lo01 = __byte_perm(v0, v1, 0x5410), hi01 = __byte_perm(v0, v1, 0x7632);
           const uint32_t lo23 = __byte_perm(v2, v3, 0x5410), hi23 = __byte_perm(v2, v3, 0x7632);
           const bool on = GP == 8 || g / GP == ti;
@@ -550,96 +555,187 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
           for (int c = 0; c < 4; c++) o[p][mt][c] += ob[p][mt][c];
     }
-    __syncwarp();
-    if (lane == 0 && i + ST < mine) issue(i + ST);  // into the stage just read
   }
-  // after an expired wait the copies still in flight land before shared memory is reused
-  if (!ok && lane == 0)
-    for (int i = done; i < mine && i < done + ST; i++) {
+
+  // Join the lanes' sums and the key tiles' columns: afterwards the lanes with 2 t < GP hold, for
+  // the query heads 2 t and 2 t + 1, the maximum m2, the sum l2 and the outputs value(p, hf, mt, c).
+  __device__ __forceinline__ void join() {
+#pragma unroll
+    for (int k = 4; k < 32; k <<= 1) {
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        l2[c] += __shfl_xor_sync(0xffffffffu, l2[c], k);
+#pragma unroll
+        for (int p = 0; p < NG; p++) ofs[p][c] += __shfl_xor_sync(0xffffffffu, ofs[p][c], k);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+      float m = m2[c];
+#pragma unroll
+      for (int k = GP / 2; k < 4; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      // a column with no key yet holds zeros (or what a NaN key left: kept)
+      const float f = m2[c] == -INFINITY ? 1.f : tc::ex2(m2[c] - m);
+      m2[c] = m;
+      l2[c] *= f;
+#pragma unroll
+      for (int k = GP / 2; k < 4; k <<= 1) l2[c] += __shfl_xor_sync(0xffffffffu, l2[c], k);
+#pragma unroll
+      for (int p = 0; p < NG; p++)
+#pragma unroll
+        for (int mt = 0; mt < 4; mt++)
+#pragma unroll
+          for (int hf = 0; hf < 2; hf++) {
+            float v = (o[p][mt][c + 2 * hf] + ofs[p][c]) * f;
+#pragma unroll
+            for (int k = GP / 2; k < 4; k <<= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+            o[p][mt][c + 2 * hf] = v;
+          }
+    }
+  }
+  // four consecutive channels p * 64 + 8 g + 4 hf .. of query head 2 t + c (after join)
+  __device__ __forceinline__ float4 value(int p, int hf, int c) const {
+    return make_float4(o[p][0][c + 2 * hf], o[p][1][c + 2 * hf], o[p][2][c + 2 * hf], o[p][3][c + 2 * hf]);
+  }
+};
+
+// Ring of a warp's blocks in shared memory: blocks first, first + stride, ... (n of them) of a run
+// that starts at base.
+template <int BLK, int ST>
+struct Ring {
+  uint8_t *mem;
+  uint64_t *bars;
+  volatile int *abort;
+  int *err;
+  uint32_t at = 0;   // blocks taken since the barriers were made
+  __device__ __forceinline__ void issue(uint32_t i, const uint8_t *src) const {
+    const uint32_t bar = tc::smem_u32(&bars[i % ST]);
+    tc::mbar_expect_tx(bar, BLK);
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            tc::smem_u32(mem + (i % ST) * BLK)),
+        "l"(src), "r"((uint32_t)BLK), "r"(bar)
+        : "memory");
+  }
+  __device__ __forceinline__ bool wait(uint32_t i) const {
+    return tc::mbar_wait(tc::smem_u32(&bars[i % ST]), (i / ST) & 1, abort, err);
+  }
+  // after an expired wait: the copies i0 .. i1 - 1, still in flight, land (or time out) before the exit
+  __device__ __forceinline__ void drain(uint32_t i0, uint32_t i1) const {
+    for (uint32_t i = i0; i < i1; i++) {
       const uint64_t t0 = tc::globaltimer();
-      while (!tc::mbar_try_wait(tc::smem_u32(&bars[warp * ST + i % ST]), (uint32_t)((i / ST) & 1)) &&
+      while (!tc::mbar_try_wait(tc::smem_u32(&bars[i % ST]), (i / ST) & 1) &&
              tc::globaltimer() - t0 < tc::WAIT_LIMIT_NS) {
       }
     }
+  }
+};
 
-  // ---- join the key tiles' columns of a query head inside the warp
-#pragma unroll
-  for (int k = 4; k < 32; k <<= 1) {
-#pragma unroll
-    for (int c = 0; c < 2; c++) {
-      l2[c] += __shfl_xor_sync(0xffffffffu, l2[c], k);
-#pragma unroll
-      for (int p = 0; p < NG; p++) ofs[p][c] += __shfl_xor_sync(0xffffffffu, ofs[p][c], k);
-    }
+// Keys of sequence b; a length outside the cache is reported and counts as none
+__device__ __forceinline__ int keys_of(const AttnArgs &a, int b, bool report) {
+  const long len = (long)a.lens[b] + a.len_add;
+  if (len < 0 || len > a.cap) {
+    if (report) raise_dev_error(a.err, DEV_BAD_INDEX);
+    return 0;
   }
-  float M2[2];
-#pragma unroll
-  for (int c = 0; c < 2; c++) {
-    float m = m2[c];
-#pragma unroll
-    for (int k = GP / 2; k < 4; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    M2[c] = m;
-    const float f = m2[c] == -INFINITY ? 0.f : tc::ex2(m2[c] - m);
-    // a column with no key yet holds zeros (or what a NaN key left: kept)
-    const float ff = m2[c] == -INFINITY ? 1.f : f;
-    l2[c] *= ff;
-#pragma unroll
-    for (int p = 0; p < NG; p++) {
-      ofs[p][c] *= ff;
-#pragma unroll
-      for (int mt = 0; mt < 4; mt++) {
-        o[p][mt][c] *= ff;
-        o[p][mt][c + 2] *= ff;
-      }
-    }
-#pragma unroll
-    for (int k = GP / 2; k < 4; k <<= 1) {
-      l2[c] += __shfl_xor_sync(0xffffffffu, l2[c], k);
-#pragma unroll
-      for (int p = 0; p < NG; p++) {
-        ofs[p][c] += __shfl_xor_sync(0xffffffffu, ofs[p][c], k);
-#pragma unroll
-        for (int mt = 0; mt < 4; mt++) {
-          o[p][mt][c] += __shfl_xor_sync(0xffffffffu, o[p][mt][c], k);
-          o[p][mt][c + 2] += __shfl_xor_sync(0xffffffffu, o[p][mt][c + 2], k);
-        }
-      }
-    }
+  return (int)len;
+}
+
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
+// Form for little work (one launch): a cluster of CTAs takes one (sequence, key head, chunk of GP
+// query heads), every CTA a contiguous share of its blocks, every warp each NW-th block of that;
+// warps join in shared memory, CTAs in distributed shared memory.
+template <typename T, int NG, int GP, int NW, int ST>
+__global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
+  using W = WarpAttn<T, NG, GP>;
+  constexpr int D = W::D, BLK = W::BLK;
+  extern __shared__ __align__(128) uint8_t ring_mem[];  // rings; then [NW][GP][D] partial outputs
+  __shared__ __align__(8) uint64_t bars[NW * ST];
+  __shared__ float sm_m[NW][GP], sm_l[NW][GP];
+  __shared__ float so[GP][D], sM[GP], sL[GP];
+  __shared__ int s_abort;
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t crank, csize;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const int item = blockIdx.x / csize;
+  const int qc = item % a.qchunks, pair = item / a.qchunks;
+  const int b = pair / a.Hkv, kvh = pair % a.Hkv;
+  const int nq = min(GP, a.G - qc * GP);
+  const int head0 = kvh * a.G + qc * GP;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NW * ST; i++) tc::mbar_init(tc::smem_u32(&bars[i]), 1);
+    tc::fence_mbar_init();
+    s_abort = 0;
   }
-  __syncthreads();  // every warp is done with the ring
-  float *part = reinterpret_cast<float *>(ring);  // [NW][GP][D]
+  __syncthreads();
+  const int nkeys = keys_of(a, b, threadIdx.x == 0);
+  const int nb = (nkeys + KV4_BLOCK - 1) / KV4_BLOCK;
+  const int per = (nb + (int)csize - 1) / (int)csize;
+  const int blk0 = min(nb, (int)crank * per), blk1 = min(nb, blk0 + per);
+  const uint8_t *base = a.data + (long)pair * (a.cap / KV4_BLOCK) * BLK;
+  const int mine = blk1 - blk0 > warp ? (blk1 - blk0 - warp + NW - 1) / NW : 0;
+  Ring<BLK, ST> ring{ring_mem + warp * ST * BLK, bars + warp * ST, &s_abort, a.err};
+  auto src = [&](int i) { return base + (long)(blk0 + warp + i * NW) * BLK; };
+  if (lane == 0)
+    for (int i = 0; i < ST && i < mine; i++) ring.issue(i, src(i));
+  W w;
+  w.start(reinterpret_cast<const T *>(a.q) + (long)b * a.ldq + (long)head0 * D, nq, a.scale_log2);
+  for (int i = 0; i < mine; i++) {
+    if (!ring.wait(i)) {
+      if (lane == 0) ring.drain(i, min(mine, i + ST));
+      break;
+    }
+    w.block(ring.mem + (i % ST) * BLK, (blk0 + warp + i * NW) * KV4_BLOCK, nkeys);
+    __syncwarp();
+    if (lane == 0 && i + ST < mine) ring.issue(i + ST, src(i + ST));  // into the stage just read
+  }
+  w.join();
+  __syncthreads();  // every warp is done with the rings
+  float *part = reinterpret_cast<float *>(ring_mem);
   if (2 * t < GP) {
 #pragma unroll
     for (int c = 0; c < 2; c++) {
       const int qh = 2 * t + c;
       if (g == 0) {
-        sm_m[warp][qh] = M2[c];
-        sm_l[warp][qh] = l2[c];
+        sm_m[warp][qh] = w.m2[c];
+        sm_l[warp][qh] = w.l2[c];
       }
 #pragma unroll
       for (int p = 0; p < NG; p++)
 #pragma unroll
-        for (int hf = 0; hf < 2; hf++) {
-          float *dst = part + (warp * GP + qh) * D + p * 64 + 8 * g + 4 * hf;
-          *reinterpret_cast<float4 *>(dst) = make_float4(
-              o[p][0][c + 2 * hf] + ofs[p][c], o[p][1][c + 2 * hf] + ofs[p][c],
-              o[p][2][c + 2 * hf] + ofs[p][c], o[p][3][c + 2 * hf] + ofs[p][c]);
-        }
+        for (int hf = 0; hf < 2; hf++)
+          *reinterpret_cast<float4 *>(part + (warp * GP + qh) * D + p * 64 + 8 * g + 4 * hf) = w.value(p, hf, c);
     }
   }
   __syncthreads();
-  // ---- join the warps
   for (int e = threadIdx.x; e < GP * D; e += NW * 32) {
     const int qh = e / D;
     float m = sm_m[0][qh];
 #pragma unroll
-    for (int w = 1; w < NW; w++) m = fmaxf(m, sm_m[w][qh]);
+    for (int k = 1; k < NW; k++) m = fmaxf(m, sm_m[k][qh]);
     float acc = 0.f, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; w++) {
-      const float f = sm_m[w][qh] == -INFINITY ? 1.f : tc::ex2(sm_m[w][qh] - m);
-      acc = fmaf(f, part[w * GP * D + e], acc);
-      l = fmaf(f, sm_l[w][qh], l);
+    for (int k = 0; k < NW; k++) {
+      const float f = sm_m[k][qh] == -INFINITY ? 1.f : tc::ex2(sm_m[k][qh] - m);
+      acc = fmaf(f, part[k * GP * D + e], acc);
+      l = fmaf(f, sm_l[k][qh], l);
     }
     so[qh][e % D] = acc;
     if (e % D == 0) {
@@ -647,7 +743,7 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
       sL[qh] = l;
     }
   }
-  // ---- join the CTAs of the cluster: every CTA writes its share of the output
+  // every CTA of the cluster writes its share of the output
   if (csize > 1) cluster_sync();
   else __syncthreads();
   const int aborted = *(volatile int *)&s_abort;
@@ -673,6 +769,262 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
       reinterpret_cast<T *>(a.out)[(long)b * a.ldo + (long)(head0 + qh) * D + e % D] = from_f<T>(res);
   }
   if (csize > 1) cluster_sync();  // shared memory that others read stays until they have
+}
+
+// Form for much work: the blocks of all items (sequence, key head, chunk of query heads) form one
+// sequence, item by item, and every warp of a grid that fills the GPU once takes an equal run of it,
+// whatever the lengths.  A warp that holds a whole item writes its output; the others leave
+// partial outputs in slot (warp + item), and kv4_join_kernel joins an item's slots, which are
+// consecutive.
+__device__ __forceinline__ int warp_incl_sum(int v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += u;
+  }
+  return v;
+}
+// blocks of all items; per_seq items a sequence
+__device__ __forceinline__ int total_blocks(const AttnArgs &a, int per_seq) {
+  int s = 0;
+  for (int i = threadIdx.x & 31; i < a.B; i += 32) s += (keys_of(a, i, false) + KV4_BLOCK - 1) / KV4_BLOCK;
+  return __reduce_add_sync(0xffffffffu, s) * per_seq;
+}
+
+template <typename T, int NG, int GP, int NW, int ST, int OCC>
+__global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
+  using W = WarpAttn<T, NG, GP>;
+  constexpr int D = W::D, BLK = W::BLK;
+  extern __shared__ __align__(128) uint8_t ring_mem[];
+  __shared__ __align__(8) uint64_t bars[NW * ST];
+  __shared__ int s_abort;
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NW * ST; i++) tc::mbar_init(tc::smem_u32(&bars[i]), 1);
+    tc::fence_mbar_init();
+    s_abort = 0;
+  }
+  if (blockIdx.x == 0 && warp == 0)
+    for (int i = lane; i < a.B; i += 32) keys_of(a, i, true);
+  __syncthreads();
+  const int gw = blockIdx.x * NW + warp;
+  const int per_seq = a.Hkv * a.qchunks;
+  const int total = total_blocks(a, per_seq);
+  const int per = (total + a.n_warps - 1) / a.n_warps;
+  const int f0 = min((long)gw * per, (long)total), f1 = min((long)f0 + per, (long)total);
+  if (f0 >= f1) return;
+  // the sequence of block f0, and the blocks before it
+  int b = 0, before = 0;
+  for (int i0 = 0, sum = 0; i0 < a.B; i0 += 32) {
+    const int n = i0 + lane < a.B ? (keys_of(a, i0 + lane, false) + KV4_BLOCK - 1) / KV4_BLOCK * per_seq : 0;
+    const int incl = sum + warp_incl_sum(n);
+    const unsigned past = __ballot_sync(0xffffffffu, incl > f0);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      b = i0 + k;
+      before = __shfl_sync(0xffffffffu, incl - n, k);
+      break;
+    }
+    sum = __shfl_sync(0xffffffffu, incl, 31);
+  }
+  // the run as segments of one item each: (b, item of the sequence, block), walked twice, by the
+  // issue of copies and, up to ST blocks behind it, by the arithmetic
+  struct Walk {
+    int b, nkeys, nb, it, blk;
+  };
+  auto enter = [&](Walk &k) {  // the first sequence from k.b on with a key
+    for (;;) {
+      k.nkeys = keys_of(a, k.b, false);
+      k.nb = (k.nkeys + KV4_BLOCK - 1) / KV4_BLOCK;
+      if (k.nb > 0) return;
+      k.b++;
+    }
+  };
+  auto src = [&](const Walk &k) {
+    return a.data + ((long)(k.b * a.Hkv + k.it / a.qchunks) * (a.cap / KV4_BLOCK) + k.blk) * BLK;
+  };
+  Walk c;
+  c.b = b;
+  enter(c);
+  c.it = (f0 - before) / c.nb;
+  c.blk = (f0 - before) % c.nb;
+  Walk ld = c;
+  Ring<BLK, ST> ring{ring_mem + warp * ST * BLK, bars + warp * ST, &s_abort, a.err};
+  const int n = f1 - f0;
+  int issued = 0;
+  auto issue_next = [&]() {
+    if (lane == 0) ring.issue(issued, src(ld));
+    issued++;
+    if (issued < n && ++ld.blk == ld.nb) {
+      ld.blk = 0;
+      if (++ld.it == per_seq) {
+        ld.it = 0;
+        ld.b++;
+        enter(ld);
+      }
+    }
+  };
+  for (int i = 0; i < ST && i < n; i++) issue_next();
+  W w;
+  bool fresh = true, whole = c.blk == 0;
+  for (int i = 0; i < n; i++) {
+    const int qc = c.it % a.qchunks, kvh = c.it / a.qchunks;
+    const int head0 = kvh * a.G + qc * GP, nq = min(GP, a.G - qc * GP);
+    if (fresh)
+      w.start(reinterpret_cast<const T *>(a.q) + (long)c.b * a.ldq + (long)head0 * D, nq, a.scale_log2);
+    fresh = false;
+    if (!ring.wait(i)) {
+      if (lane == 0) ring.drain(i, issued);
+      return;
+    }
+    w.block(ring.mem + (i % ST) * BLK, c.blk * KV4_BLOCK, c.nkeys);
+    __syncwarp();
+    if (issued < n) issue_next();  // into the stage just read
+    const bool end = c.blk + 1 == c.nb;
+    if (end || i + 1 == n) {
+      w.join();
+      if (2 * t < GP) {
+        if (whole && end) {
+          T *dst = reinterpret_cast<T *>(a.out) + (long)c.b * a.ldo + (long)head0 * D;
+#pragma unroll
+          for (int k = 0; k < 2; k++)
+            if (2 * t + k < nq) {
+              const float inv = 1.f / w.l2[k];
+#pragma unroll
+              for (int p = 0; p < NG; p++) {
+                const float4 u = w.value(p, 0, k), v = w.value(p, 1, k);
+                const float r[8] = {u.x * inv, u.y * inv, u.z * inv, u.w * inv, v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+                store8(dst + (2 * t + k) * D + p * 64 + 8 * g, r);
+              }
+            }
+        } else {
+          float *dst = a.part + (long)(gw + c.b * per_seq + c.it) * GP * (D + 4);
+#pragma unroll
+          for (int k = 0; k < 2; k++)
+            if (2 * t + k < nq) {
+              float *d = dst + (2 * t + k) * (D + 4);
+#pragma unroll
+              for (int p = 0; p < NG; p++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++)
+                  *reinterpret_cast<float4 *>(d + p * 64 + 8 * g + 4 * hf) = w.value(p, hf, k);
+              if (g == 0) *reinterpret_cast<float2 *>(d + D) = make_float2(w.m2[k], w.l2[k]);
+            }
+        }
+      }
+      fresh = true;
+      whole = true;
+    }
+    if (i + 1 < n && ++c.blk == c.nb) {
+      c.blk = 0;
+      if (++c.it == per_seq) {
+        c.it = 0;
+        c.b++;
+        enter(c);
+      }
+    }
+  }
+}
+
+// Join the slots of an item's query head: eight warps take every eighth slot, a lane D / 32
+// channels, then the warps join in shared memory.  Items that one warp held are done; items without
+// a key get zeros.
+template <typename T, int D, int GP>
+__global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a) {
+  constexpr int NW = 8, C = D / 32;
+  __shared__ float so[NW][D], sm[NW], sl[NW];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_seq = a.Hkv * a.qchunks;
+  const int b = blockIdx.x / (a.Hkv * a.G), head = blockIdx.x % (a.Hkv * a.G);
+  const int kvh = head / a.G, qh = head % a.G;
+  const int it = kvh * a.qchunks + qh / GP;
+  int sum = 0, upto = 0;  // blocks of all sequences, and of those before b
+  for (int i = lane; i < a.B; i += 32) {
+    const int nb = (keys_of(a, i, false) + KV4_BLOCK - 1) / KV4_BLOCK;
+    sum += nb;
+    upto += i < b ? nb : 0;
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum) * per_seq;
+  upto = __reduce_add_sync(0xffffffffu, upto) * per_seq;
+  const int nb = (keys_of(a, b, false) + KV4_BLOCK - 1) / KV4_BLOCK;
+  T *dst = reinterpret_cast<T *>(a.out) + (long)b * a.ldo + (long)head * D;
+  if (nb == 0) {
+    for (int e = threadIdx.x; e < D; e += 256) dst[e] = from_f<T>(0.f);
+    return;
+  }
+  const int per = (sum + a.n_warps - 1) / a.n_warps;
+  const int s = upto + it * nb;
+  const int w0 = s / per, w1 = (s + nb - 1) / per;
+  if (w0 == w1) return;
+  const float *part = a.part + ((long)(w0 + b * per_seq + it) * GP + qh % GP) * (D + 4);
+  const long step = (long)GP * (D + 4);
+  const int n = w1 - w0 + 1;
+  float m = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; c++) acc[c] = 0.f;
+  // four slots a step, their loads in flight together
+  for (int i = warp; i < n; i += 4 * NW) {
+    float2 ml[4];
+    float v[4][C];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int j = i + k * NW;
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int c = 0; c < C; c++) v[k][c] = 0.f;
+      if (j < n) {
+        const float *p = part + j * step;
+        ml[k] = *reinterpret_cast<const float2 *>(p + D);
+        if constexpr (C == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(p + 4 * lane);
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(p + 2 * lane);
+          v[k][0] = x.x; v[k][1] = x.y;
+        }
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < 4; k++) mn = fmaxf(mn, ml[k].x);
+    const float al = m == -INFINITY ? 1.f : tc::ex2(m - mn);
+    l *= al;
+#pragma unroll
+    for (int c = 0; c < C; c++) acc[c] *= al;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float f = ml[k].x == -INFINITY ? 1.f : tc::ex2(ml[k].x - mn);
+      l = fmaf(f, ml[k].y, l);
+#pragma unroll
+      for (int c = 0; c < C; c++) acc[c] = fmaf(f, v[k][c], acc[c]);
+    }
+    m = mn;
+  }
+#pragma unroll
+  for (int c = 0; c < C; c++) so[warp][C * lane + c] = acc[c];
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < D; e += 256) {
+    float M = sm[0];
+#pragma unroll
+    for (int k = 1; k < NW; k++) M = fmaxf(M, sm[k]);
+    float r = 0.f, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; k++) {
+      const float f = sm[k] == -INFINITY ? 1.f : tc::ex2(sm[k] - M);
+      r = fmaf(f, so[k][e], r);
+      L = fmaf(f, sl[k], L);
+    }
+    dst[e] = from_f<T>(r / L);
+  }
 }
 
 template <typename K, typename... A>
@@ -719,22 +1071,60 @@ dim3 row_grid(const RowArgs &a) {
   return dim3((a.n_rows + ROWS_T - 1) / ROWS_T, (a.Hkv * a.ng + 7) / 8, 2);
 }
 
-template <typename T, int NG, int GP, int TERMS, int NW, int ST>
-int launch_attn(const AttnArgs &a, int pairs, int cluster, cudaStream_t s, LaunchOpt o) {
-  using C = AttnCfg<NG, GP, TERMS, NW, ST>;
-  const long ctas = (long)pairs * a.qchunks * cluster;
-  if (ctas > 0x7fffffffL) return DREAMER_ERR_UNSUPPORTED;
-  return launch(kv4_attn_kernel<T, NG, GP, TERMS, NW, ST>, dim3((unsigned)ctas), dim3(NW * 32), C::SMEM,
-                cluster, s, o, a);
+int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return 148;
+  return sms;
 }
 
-template <typename T, int NG, int TERMS>
-int dispatch_attn(AttnArgs a, int pairs, int cluster, cudaStream_t s, LaunchOpt o) {
-  const int gp = a.G <= 2 ? 2 : a.G <= 4 ? 4 : 8;
-  a.qchunks = (a.G + gp - 1) / gp;
-  if (gp == 2) return launch_attn<T, NG, 2, TERMS, 4, 3>(a, pairs, cluster, s, o);
-  if (gp == 4) return launch_attn<T, NG, 4, TERMS, 4, 3>(a, pairs, cluster, s, o);
-  return launch_attn<T, NG, 8, TERMS, 4, 3>(a, pairs, cluster, s, o);
+// Warps a CTA, ring stages and CTAs an SM of the split form
+template <typename T, int NG> struct SplitCfg {
+  static constexpr int NW = 4;
+  static constexpr int ST = NG == 1 ? 3 : 2;
+  static constexpr int OCC = sizeof(T) == 4 ? 2 : NG == 1 ? 4 : 3;
+};
+
+int heads_a_chunk(int G) { return G <= 2 ? 2 : G <= 4 ? 4 : 8; }
+
+// The split form pays where one cluster launch would leave warps with several blocks each
+bool use_split(long items, int nblk) { return items * nblk > 4096; }
+
+template <typename T, int NG, int GP>
+int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
+  using W = WarpAttn<T, NG, GP>;
+  a.qchunks = (a.G + GP - 1) / GP;
+  const long items = (long)a.B * a.Hkv * a.qchunks;
+  const int nblk = a.cap / KV4_BLOCK;
+  if (items * nblk >= 0x7fffffffL) return DREAMER_ERR_UNSUPPORTED;
+  if (use_split(items, nblk)) {
+    using C = SplitCfg<T, NG>;
+    const int grid = device_sms() * C::OCC;
+    a.n_warps = grid * C::NW;
+    const int rc = launch(kv4_split_kernel<T, NG, GP, C::NW, C::ST, C::OCC>, dim3(grid), dim3(C::NW * 32),
+                          C::NW * C::ST * W::BLK, 1, s, o, a);
+    if (rc) return rc;
+    LaunchOpt j;
+    j.pdl = true;  // the split kernel precedes it on the stream
+    return launch(kv4_join_kernel<T, W::D, GP>, dim3((unsigned)(a.B * a.Hkv * a.G)), dim3(256), 0, 1, s, j, a);
+  }
+  constexpr int NW = 4, ST = 3;
+  // CTAs of an item: at least a block a warp, and no more than fill the GPU
+  int cluster = 1;
+  while (cluster < 8 && items * cluster < 148 * 2 && nblk > NW * cluster) cluster *= 2;
+  constexpr int part = NW * GP * W::D * 4, rings = NW * ST * W::BLK;
+  return launch(kv4_attn_kernel<T, NG, GP, NW, ST>, dim3((unsigned)(items * cluster)), dim3(NW * 32),
+                rings > part ? rings : part, cluster, s, o, a);
+}
+
+template <typename T, int NG>
+int dispatch_attn(const AttnArgs &a, cudaStream_t s, LaunchOpt o) {
+  switch (heads_a_chunk(a.G)) {
+    case 2: return launch_attn<T, NG, 2>(a, s, o);
+    case 4: return launch_attn<T, NG, 4>(a, s, o);
+    default: return launch_attn<T, NG, 8>(a, s, o);
+  }
 }
 
 }  // namespace
@@ -761,15 +1151,17 @@ int kv4_attn(const Kv4Cache &c, const Kv4Attn &t, cudaStream_t s, LaunchOpt o) {
   a.lens = t.lens; a.len_add = t.len_add;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   a.err = t.err;
-  const int pairs = c.B * c.Hkv;
-  // CTAs of a (sequence, key head): enough for several waves, at least four blocks each
-  const int nblk = c.cap / KV4_BLOCK;
-  int cluster = 1;
-  while (cluster < 16 && (long)pairs * cluster < 148 * 8 && nblk / (2 * cluster) >= 4) cluster *= 2;
-  const bool f32 = t.dtype == 0;
-  if (c.d == 64)
-    return f32 ? dispatch_attn<float, 1, 3>(a, pairs, cluster, s, o) : dispatch_attn<bf16, 1, 1>(a, pairs, cluster, s, o);
-  return f32 ? dispatch_attn<float, 2, 3>(a, pairs, cluster, s, o) : dispatch_attn<bf16, 2, 1>(a, pairs, cluster, s, o);
+  a.part = (float *)t.workspace;
+  if (c.d == 64) return t.dtype == 0 ? dispatch_attn<float, 1>(a, s, o) : dispatch_attn<bf16, 1>(a, s, o);
+  return t.dtype == 0 ? dispatch_attn<float, 2>(a, s, o) : dispatch_attn<bf16, 2>(a, s, o);
+}
+
+long kv4_attn_workspace(const Kv4Cache &c, int Hq, bool any_capacity) {
+  const int G = Hq / c.Hkv, gp = heads_a_chunk(G);
+  const long items = (long)c.B * c.Hkv * ((G + gp - 1) / gp);
+  if (!any_capacity && !use_split(items, c.cap / KV4_BLOCK)) return 0;
+  const long warps = (long)device_sms() * 16;  // of either type
+  return (warps + items) * gp * (c.d + 4) * (long)sizeof(float);
 }
 
 }  // namespace ops
@@ -829,9 +1221,16 @@ extern "C" int dreamer_kv4_load(const dreamer_kv4_cache *c, void *k, int64_t ldk
                        (cudaStream_t)stream);
 }
 
+extern "C" int64_t dreamer_attn_kv4_workspace(const dreamer_kv4_cache *c, int n_heads) {
+  if (!c || c->batch < 1 || c->n_kv_heads < 1 || n_heads < 1 || n_heads % c->n_kv_heads ||
+      !dreamer_kv4_bytes(c->batch, c->n_kv_heads, c->head_dim, c->capacity))
+    return 0;
+  return ops::kv4_attn_workspace(to_cache(c), n_heads);
+}
+
 extern "C" int dreamer_attn_kv4(const dreamer_kv4_cache *c, const void *q, int64_t ldq, void *out, int64_t ldo,
-                                const int32_t *lens, int n_heads, int dtype, float scale, int32_t *status,
-                                dreamer_stream stream) {
+                                const int32_t *lens, int n_heads, int dtype, float scale, void *workspace,
+                                int64_t workspace_bytes, int32_t *status, dreamer_stream stream) {
   const int rc = check_cache(c);
   if (rc) return rc;
   if (!q || !out || !lens || n_heads < 1 || n_heads % c->n_kv_heads || (dtype != 0 && dtype != 1) ||
@@ -840,6 +1239,8 @@ extern "C" int dreamer_attn_kv4(const dreamer_kv4_cache *c, const void *q, int64
   const int es = dtype == 0 ? 4 : 2;
   const int64_t w = (int64_t)n_heads * c->head_dim;
   if (!al16(q) || !al16(out) || ldq < w || ldo < w || (ldq * es) % 16 || (ldo * es) % 16) return DREAMER_ERR_ARG;
-  return ops::kv4_attn(to_cache(c), ops::Kv4Attn{q, ldq, out, ldo, lens, 0, n_heads, dtype, scale, status},
+  const int64_t need = ops::kv4_attn_workspace(to_cache(c), n_heads);
+  if (need > 0 && (!workspace || !al16(workspace) || workspace_bytes < need)) return DREAMER_ERR_ARG;
+  return ops::kv4_attn(to_cache(c), ops::Kv4Attn{q, ldq, out, ldo, lens, 0, n_heads, dtype, scale, workspace, status},
                        (cudaStream_t)stream);
 }

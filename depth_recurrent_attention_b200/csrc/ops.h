@@ -68,8 +68,11 @@ struct Kv4Attn {
   int Hq;
   int dtype;
   float scale;
+  void *workspace;  // kv4_attn_workspace bytes
   int *err;
 };
+// bytes of the workspace (0: none needed); any_capacity: whatever c.cap is
+long kv4_attn_workspace(const Kv4Cache &c, int Hq, bool any_capacity = false);
 int kv4_attn(const Kv4Cache &c, const Kv4Attn &a, cudaStream_t s, LaunchOpt o = LaunchOpt());
 
 }  // namespace ops

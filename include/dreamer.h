@@ -283,10 +283,17 @@ int dreamer_kv4_load(const dreamer_kv4_cache *cache, void *k, int64_t ldk, void 
  * and a sequence with lens[b] = 0 gets zeros.  q, out: [batch] rows of n_heads * head_dim of
  * dtype (out may be q); lens [batch] int32; n_heads a multiple of n_kv_heads.  Sums, softmax
  * and products are float32, the weights of the output product bfloat16 for bfloat16 (float32
- * in three terms for float32).  What lies in the cache behind lens[b] is not used.          */
+ * in three terms for float32).  What lies in the cache behind lens[b] is not used.
+ * workspace: device memory of at least dreamer_attn_kv4_workspace() bytes (NULL where that is 0),
+ * 16-byte aligned, contents of no matter; calls that may run at the same time need one each.  */
 int dreamer_attn_kv4(const dreamer_kv4_cache *cache, const void *q, int64_t ldq, void *out,
                      int64_t ldo, const int32_t *lens, int n_heads, int dtype, float scale,
-                     int32_t *status, dreamer_stream stream);
+                     void *workspace, int64_t workspace_bytes, int32_t *status,
+                     dreamer_stream stream);
+
+/* Workspace bytes of dreamer_attn_kv4 on the current device (0 for little work, and for
+ * arguments that it refuses).                                                               */
+int64_t dreamer_attn_kv4_workspace(const dreamer_kv4_cache *cache, int n_heads);
 
 /* dreamer_core_forward over packed prompts of different lengths: n_seq prompts with tokens
  * cu_seqlens[i] .. cu_seqlens[i+1]-1 (int32 [n_seq+1], device; cu_seqlens[0] = 0, not decreasing,

@@ -73,6 +73,8 @@ def attend(data, d, q, lens, scale, out_eps):
                                         |m + 8 s| sum |q|) at most over the keys, times log 2 rounding
                                         and the exponential (2^-21), on weights and on their sum
       n u sum_j w_j |v_j|               the sums over n keys, of weights and of products
+    bfloat16 (out_eps 2^-8) scores are taken with q in steps of its plane's largest |q| / 32512: each
+    q is off by half a step at most, so E has scale sum over planes of (half a step) sum s c more.
     """
     codes, s, m = unpack(data, d)
     B, Hq, _ = q.shape
@@ -96,6 +98,8 @@ def attend(data, d, q, lens, scale, out_eps):
             o = w @ v
             aq = np.abs(qq).reshape(-1, 64)
             e = (np.abs(kc - 8) * ks[..., None] * aq).sum((1, 2)) + (np.abs(km + 8 * ks) * aq.sum(-1)).sum(1)
+            if out_eps == 2.0 ** -8:
+                e = e + (aq.max(-1) / 65024 * (kc * ks[..., None]).sum(-1)).sum(-1) / ((d + 8) * u)
             E = (d + 8) * u * abs(scale) * e.max() + 2.0 ** -21 + u * (1 + np.abs(z - z.max()).max())
             absv = w @ np.abs(v) + w @ (np.abs(vm + 8 * vs)[..., None] + np.zeros((1, 1, 64))).reshape(n, d)
             spread = w @ (np.abs(vc - 8) * vs[..., None]).reshape(n, d)

@@ -43,7 +43,7 @@ def test_caches_that_are_refused(L, kw, rc):
     assert L.dreamer_kv4_store(c, P, 1 << 12, P, 1 << 12, P, P, 4, 1, None, None) == rc
     assert L.dreamer_kv4_load(c, P, 1 << 12, P, 1 << 12, P, P, 4, 1, 0, None, None) == rc
     assert L.dreamer_attn_kv4(c, P, 1 << 12, P, 1 << 12, P, 4 if kw.get("n_kv_heads") != 64 else 64, 1, 0.125,
-                              None, None) == rc
+                              P, 1 << 40, None, None) == rc
 
 
 @pytest.mark.parametrize("at,value", [
@@ -62,7 +62,7 @@ def test_rows_that_are_refused(L, at, value):
     (7, 2), (8, float("nan")), (8, float("inf")),
 ])
 def test_attention_calls_that_are_refused(L, at, value):
-    a = [_cache(), P, 256, P, 256, P, 4, 1, 0.125, None, None]
+    a = [_cache(), P, 256, P, 256, P, 4, 1, 0.125, None, 0, None, None]
     a[at] = value
     assert L.dreamer_attn_kv4(*a) == ARG
     assert L.dreamer_attn_kv4(None, *a[1:]) == ARG
@@ -114,3 +114,14 @@ def test_the_packed_binding_refuses_tensors_of_the_host():
     x = torch.zeros((4, 1, 64))
     with pytest.raises(ValueError):
         attn_packed(x, x, x, torch.zeros(2, dtype=torch.int32))
+
+
+def test_workspace_of_attention(L):
+    small, large = _cache(), _cache(batch=64, n_kv_heads=16, capacity=8192)
+    assert L.dreamer_attn_kv4_workspace(small, 4) == 0
+    need = L.dreamer_attn_kv4_workspace(large, 16)
+    assert need > 0 and L.dreamer_attn_kv4_workspace(large, 17) == 0 and L.dreamer_attn_kv4_workspace(None, 16) == 0
+    a = [large, P, 1 << 12, P, 1 << 12, P, 16, 1, 0.125, None, 0, None, None]
+    for ws, n in ((None, need), (P, need - 1), (P + 8, need)):
+        a[9], a[10] = ws, n
+        assert L.dreamer_attn_kv4(*a) == ARG
