@@ -209,14 +209,15 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
 //   scores   A = 16 keys x channels of K codes, B = channels x 8 columns of q
 //   output   A = 16 channels x 16 keys of V codes, B = keys x 8 columns of weights
 // What bounds it is turning nibbles into operands (the integer pipe), so
-//   - bfloat16 scores run on 8-bit integer products (m16n8k32): a mask and a shift make four
-//     codes a word, and q enters as a 16-bit fixed-point number of its plane's largest |q|, in two
-//     signed bytes; the integer sums are exact, a score is off by about 2^-16 of the largest product,
-//     far below the bf16 rounding of the weights;
-//   - float32 scores, and the output products, take a code as the bf16 number c - 8, exact:
-//     (0x4300 | c) is 128 + c; float32 operands enter in three bf16 terms.
-// With value = s c + m a score is s (q . c) + m sum(q); a weight p enters the output product as p s,
-// the offsets as one sum of p (m + 8 s) a plane.
+//   - bfloat16 runs on 8-bit integer products (m16n8k32): a mask and a shift make four codes a word.
+//     q enters as a 16-bit fixed-point number of its plane's largest |q|, in two signed bytes, a weight
+//     p s as one of its column's largest in the block, in two unsigned bytes; the integer sums are
+//     exact.  Both are finer than the bf16 rounding of q, and of the output (2^-16 and 2^-17 of the
+//     largest against half a step of 2^-8);
+//   - float32 takes a code as the bf16 number c - 8, exact ((0x4300 | c) is 128 + c), and its operands
+//     in three bf16 terms.
+// With value = s c + m a score is s (q . c) + m sum(q), and the offsets enter the output as one sum of
+// p m a plane.
 // A column is (16-key tile of a supertile, query head): GP = 2, 4 or 8 columns hold the query heads
 // that share a key head, and 8 / GP key tiles share one accumulator, each with q in its own columns
 // and zeros elsewhere.  So one exponential a (key, query head) is computed also where a key head has
@@ -247,13 +248,21 @@ __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// unsigned bytes times signed bytes, 32-bit integer sums
-__device__ __forceinline__ void mma16832(int *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// unsigned bytes times signed (SB) or unsigned bytes, 32-bit integer sums: d = c + a b
+template <bool SB>
+__device__ __forceinline__ void mma16832(int *d, const uint32_t *a, uint32_t b0, uint32_t b1, const int *c) {
+  if constexpr (SB)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
 }
 // transpose of an 8 x 8 matrix of 16-bit values held as mma fragments
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -281,8 +290,7 @@ constexpr float MAGIC_F = 12582912.f;
 // The attention of one warp over blocks of one (sequence, key head) for up to GP query heads.
 template <typename T, int NG, int GP>
 struct WarpAttn {
-  static constexpr bool INT = sizeof(T) == 2;       // scores on integer products
-  static constexpr int TERMS = sizeof(T) == 2 ? 1 : 3;  // bf16 terms of a weight (and of a float32 q)
+  static constexpr bool INT = sizeof(T) == 2;       // products on bytes (else in three bf16 terms)
   static constexpr int D = NG * 64;
   static constexpr int NTI = 8 / GP;                // key tiles that share an accumulator
   static constexpr int NSUP = 4 / NTI;              // accumulators of a block
@@ -292,14 +300,17 @@ struct WarpAttn {
   uint32_t qf[NG][QR];
   float qs[NG][2];     // sum(q) of this lane's columns 2t, 2t + 1, times scale_log2
   float qi[NG][2];     // INT: the columns' fixed-point step, times scale_log2
-  float o[NG][4][4];   // [plane][channel tile][c]: channels 8g + mt, 8g + 4 + mt, columns 2t, 2t + 1
-  float ofs[NG][2];    // sum of p (m + 8 s)
+  float o[NG][4][4];   // [plane][channel tile][c]: c >> 1 channel, c & 1 column 2t or 2t + 1
+  float ofs[NG][2];    // sum of p m (of p (m + 8 s) where codes enter as c - 8)
   float m2[2], l2[2];
+  uint32_t sel[NTI];   // 1 for the tile of column g, else 0
 
   // q as B fragments: column g is query head g % GP; a lane holds channels 16 t .. 16 t + 15 of a plane
   __device__ __forceinline__ void start(const T *q, int nq, float scale_log2) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int qh = g % GP;
+#pragma unroll
+    for (int ti = 0; ti < NTI; ti++) sel[ti] = g / GP == ti ? 1u : 0u;
     const T *qp = q + (long)(qh < nq ? qh : 0) * D + 16 * t;
 #pragma unroll
     for (int p = 0; p < NG; p++) {
@@ -372,25 +383,34 @@ struct WarpAttn {
     }
   }
 
+  // an operand register in its own columns' tile, zero in the others: a product, which the busy integer
+  // pipe does not see
+  __device__ __forceinline__ uint32_t in_tile(uint32_t v, int ti) const {
+    if constexpr (GP == 8) return v;
+    uint32_t r;
+    asm("mul.lo.u32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(sel[ti]));
+    return r;
+  }
+
   // q . c (integer form: c; float form: c - 8) of supertile sp in plane p for this lane's two keys and
   // columns, to be scaled by qi and s
   __device__ __forceinline__ void products(const uint8_t *blk, int sp, int p, float *f) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint8_t *kr = blk + p * PLANE + (sp * NTI * 16 + perm_row(g)) * 32 + 8 * t;
     if constexpr (INT) {
-      int hi[4] = {MAGIC, MAGIC, MAGIC, MAGIC}, lo[4] = {MAGIC, MAGIC, MAGIC, MAGIC};
+      const int start[4] = {MAGIC, MAGIC, MAGIC, MAGIC};
+      int hi[4], lo[4];
 #pragma unroll
       for (int ti = 0; ti < NTI; ti++) {
         const uint2 w0 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32);
         const uint2 w1 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32 + 8 * 32);
-        const bool on = GP == 8 || g / GP == ti;
         const uint32_t ww0[2] = {w0.x, w0.y}, ww1[2] = {w1.x, w1.y};
 #pragma unroll
         for (int w = 0; w < 2; w++) {
           const uint32_t a[4] = {ww0[w] & 0x0f0f0f0fu, ww1[w] & 0x0f0f0f0fu, (ww0[w] >> 4) & 0x0f0f0f0fu,
                                  (ww1[w] >> 4) & 0x0f0f0f0fu};
-          mma16832(hi, a, on ? qf[p][4 * w] : 0u, on ? qf[p][4 * w + 2] : 0u);
-          mma16832(lo, a, on ? qf[p][4 * w + 1] : 0u, on ? qf[p][4 * w + 3] : 0u);
+          mma16832<true>(hi, a, in_tile(qf[p][4 * w], ti), in_tile(qf[p][4 * w + 2], ti), ti + w == 0 ? start : hi);
+          mma16832<true>(lo, a, in_tile(qf[p][4 * w + 1], ti), in_tile(qf[p][4 * w + 3], ti), ti + w == 0 ? start : lo);
         }
       }
 #pragma unroll
@@ -420,10 +440,18 @@ struct WarpAttn {
   }
 
   // One block in shared memory: keys key0 .. key0 + 63, of which those below nkeys exist
-  __device__ __forceinline__ void block(const uint8_t *blk, int key0, int nkeys) {
+  __device__ __forceinline__ void block(uint8_t *blk, int key0, int nkeys) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int my_key = ((2 * t) / GP) * 16 + perm_row(g);  // in a supertile: this lane's keys my_key (+ 8)
     const bool tail = key0 + KV4_BLOCK > nkeys;
+    if (tail) {  // what lies behind the last key may be anything: its values count as zero
+      for (int k = lane; k < KV4_BLOCK; k += 32)
+        if (key0 + k >= nkeys)
+#pragma unroll
+          for (int p = 0; p < NG; p++) *reinterpret_cast<uint32_t *>(blk + 2 * NG * PLANE + (NG + p) * PAIRS + k * 4) = 0;
+      tc::fence_proxy_async();  // the next copy into this stage comes after these writes
+      __syncwarp();
+    }
     float x[NSUP][4];
 #pragma unroll
     for (int sp = 0; sp < NSUP; sp++) {
@@ -441,7 +469,10 @@ struct WarpAttn {
         x[sp][2] = p == 0 ? y2 : x[sp][2] + y2;
         x[sp][3] = p == 0 ? y3 : x[sp][3] + y3;
       }
-      if (tail) {
+    }
+    if (tail) {
+#pragma unroll
+      for (int sp = 0; sp < NSUP; sp++) {
         const int key = key0 + sp * NTI * 16 + my_key;
         if (key >= nkeys) x[sp][0] = x[sp][1] = -INFINITY;
         if (key + 8 >= nkeys) x[sp][2] = x[sp][3] = -INFINITY;
@@ -451,8 +482,8 @@ struct WarpAttn {
     float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
 #pragma unroll
     for (int sp = 1; sp < NSUP; sp++) {
-      mx0 = fmaxf(mx0, fmaxf(x[sp][0], x[sp][2]));
-      mx1 = fmaxf(mx1, fmaxf(x[sp][1], x[sp][3]));
+      mx0 = max3f(mx0, x[sp][0], x[sp][2]);
+      mx1 = max3f(mx1, x[sp][1], x[sp][3]);
     }
     if (__any_sync(0xffffffffu, mx0 > m2[0] + 8.f || mx1 > m2[1] + 8.f)) {
 #pragma unroll
@@ -480,81 +511,156 @@ struct WarpAttn {
         }
       }
     }
-    const float r0 = m2[0] == -INFINITY ? 0.f : m2[0], r1 = m2[1] == -INFINITY ? 0.f : m2[1];
-    float ob[NG][4][4];  // TERMS > 1: the block's own sums, added in 32-bit rounding to nearest
-    if (TERMS > 1) {
+    {
+      const float r0 = m2[0] == -INFINITY ? 0.f : m2[0], r1 = m2[1] == -INFINITY ? 0.f : m2[1];
 #pragma unroll
-      for (int p = 0; p < NG; p++)
-#pragma unroll
-        for (int mt = 0; mt < 4; mt++)
-#pragma unroll
-          for (int c = 0; c < 4; c++) ob[p][mt][c] = 0.f;
-    }
-    const int pv0 = perm_row(2 * t) * 32 + 4 * g, pv1 = perm_row(2 * t + 1) * 32 + 4 * g;
-#pragma unroll
-    for (int sp = 0; sp < NSUP; sp++) {
-      const float p0 = tc::ex2(x[sp][0] - r0), p1 = tc::ex2(x[sp][1] - r1);
-      const float p2 = tc::ex2(x[sp][2] - r0), p3 = tc::ex2(x[sp][3] - r1);
-      l2[0] += p0 + p2;
-      l2[1] += p1 + p3;
-#pragma unroll
-      for (int p = 0; p < NG; p++) {
-        const uint8_t *vp = blk + 2 * NG * PLANE + (NG + p) * PAIRS + (sp * NTI * 16 + my_key) * 4;
-        float2 s0 = pair_at(vp), s1 = pair_at(vp + 8 * 4);
-        if (tail) {  // what lies behind the last key may be anything
-          const int key = key0 + sp * NTI * 16 + my_key;
-          if (key >= nkeys) s0 = make_float2(0.f, 0.f);
-          if (key + 8 >= nkeys) s1 = make_float2(0.f, 0.f);
-        }
-        const float z0 = fmaf(8.f, s0.x, s0.y), z1 = fmaf(8.f, s1.x, s1.y);
-        ofs[p][0] = fmaf(p0, z0, fmaf(p2, z1, ofs[p][0]));
-        ofs[p][1] = fmaf(p1, z0, fmaf(p3, z1, ofs[p][1]));
-        uint32_t bq[TERMS][2];  // weights as B fragments: column g, keys perm(2t), perm(2t + 1) (+ 8)
-        float y0 = p0 * s0.x, y1 = p1 * s0.x, y2 = p2 * s1.x, y3 = p3 * s1.x;
-#pragma unroll
-        for (int k = 0; k < TERMS; k++) {
-          const uint32_t h0 = bf2_pack_rn(y0, y1), h1 = bf2_pack_rn(y2, y3);
-          bq[k][0] = transpose8(h0);
-          bq[k][1] = transpose8(h1);
-          if (k + 1 < TERMS) {
-            y0 -= __uint_as_float(h0 << 16);
-            y1 -= __uint_as_float(h0 & 0xffff0000u);
-            y2 -= __uint_as_float(h1 << 16);
-            y3 -= __uint_as_float(h1 & 0xffff0000u);
-          }
-        }
-#pragma unroll
-        for (int ti = 0; ti < NTI; ti++) {
-          const uint8_t *vr = blk + (NG + p) * PLANE + (sp * NTI + ti) * 16 * 32;
-          const uint32_t v0 = *reinterpret_cast<const uint32_t *>(vr + pv0);
-          const uint32_t v1 = *reinterpret_cast<const uint32_t *>(vr + pv1);
-          const uint32_t v2 = *reinterpret_cast<const uint32_t *>(vr + pv0 + 8 * 32);
-          const uint32_t v3 = *reinterpret_cast<const uint32_t *>(vr + pv1 + 8 * 32);
-          const uint32_t lo01 = __byte_perm(v0, v1, 0x5410), hi01 = __byte_perm(v0, v1, 0x7632);
-          const uint32_t lo23 = __byte_perm(v2, v3, 0x5410), hi23 = __byte_perm(v2, v3, 0x7632);
-          const bool on = GP == 8 || g / GP == ti;
-          auto tile = [&](auto mtag) {
-            constexpr int mt = decltype(mtag)::value;
-            const uint32_t f[4] = {codes2<mt>(lo01), codes2<mt>(hi01), codes2<mt>(lo23), codes2<mt>(hi23)};
-#pragma unroll
-            for (int k = TERMS - 1; k >= 0; k--)
-              mma16816(TERMS > 1 ? ob[p][mt] : o[p][mt], f, on ? bq[k][0] : 0u, on ? bq[k][1] : 0u);
-          };
-          tile(std::integral_constant<int, 0>());
-          tile(std::integral_constant<int, 1>());
-          tile(std::integral_constant<int, 2>());
-          tile(std::integral_constant<int, 3>());
-        }
+      for (int sp = 0; sp < NSUP; sp++) {
+        x[sp][0] = tc::ex2(x[sp][0] - r0);
+        x[sp][1] = tc::ex2(x[sp][1] - r1);
+        x[sp][2] = tc::ex2(x[sp][2] - r0);
+        x[sp][3] = tc::ex2(x[sp][3] - r1);
+        l2[0] += x[sp][0] + x[sp][2];
+        l2[1] += x[sp][1] + x[sp][3];
       }
     }
-    if (TERMS > 1) {
 #pragma unroll
-      for (int p = 0; p < NG; p++)
-#pragma unroll
-        for (int mt = 0; mt < 4; mt++)
-#pragma unroll
-          for (int c = 0; c < 4; c++) o[p][mt][c] += ob[p][mt][c];
+    for (int p = 0; p < NG; p++) {
+      if constexpr (INT) out_int(blk, p, my_key, x);
+      else out_float(blk, p, my_key, x);
     }
+  }
+
+  // the four words (8 channels 8g .. 8g + 7 each) of a V tile's keys perm(2t), perm(2t + 1), (+ 8)
+  __device__ __forceinline__ void v_words(const uint8_t *blk, int p, int tile, uint32_t *v) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint8_t *vr = blk + (NG + p) * PLANE + tile * 16 * 32 + 4 * g;
+    v[0] = *reinterpret_cast<const uint32_t *>(vr + perm_row(2 * t) * 32);
+    v[1] = *reinterpret_cast<const uint32_t *>(vr + perm_row(2 * t + 1) * 32);
+    v[2] = *reinterpret_cast<const uint32_t *>(vr + perm_row(2 * t) * 32 + 8 * 32);
+    v[3] = *reinterpret_cast<const uint32_t *>(vr + perm_row(2 * t + 1) * 32 + 8 * 32);
+  }
+
+  // o += weights x values of plane p on integer products: the weights p s of a column as 16-bit
+  // fixed-point numbers of their largest in the block, in two bytes (off by 2^-17 of the largest), codes as
+  // they are.  The sums are exact; o holds channels 8g + 2 mt and 8g + 2 mt + 1.
+  __device__ __forceinline__ void out_int(const uint8_t *blk, int p, int my_key, const float (*x)[4]) {
+    float y[NSUP][4], t0 = 0.f, t1 = 0.f;
+#pragma unroll
+    for (int sp = 0; sp < NSUP; sp++) {
+      const uint8_t *vp = blk + 2 * NG * PLANE + (NG + p) * PAIRS + (sp * NTI * 16 + my_key) * 4;
+      const float2 s0 = pair_at(vp), s1 = pair_at(vp + 8 * 4);
+      ofs[p][0] = fmaf(x[sp][0], s0.y, fmaf(x[sp][2], s1.y, ofs[p][0]));
+      ofs[p][1] = fmaf(x[sp][1], s0.y, fmaf(x[sp][3], s1.y, ofs[p][1]));
+      y[sp][0] = x[sp][0] * s0.x;
+      y[sp][1] = x[sp][1] * s0.x;
+      y[sp][2] = x[sp][2] * s1.x;
+      y[sp][3] = x[sp][3] * s1.x;
+      t0 = max3f(t0, y[sp][0], y[sp][2]);
+      t1 = max3f(t1, y[sp][1], y[sp][3]);
+    }
+#pragma unroll
+    for (int k = 4; k < 32; k <<= 1) {
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, k));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, k));
+    }
+    const float i0 = t0 >= 0x1p-110f ? __fdividef(65535.f, t0) : 0.f;
+    const float i1 = t1 >= 0x1p-110f ? __fdividef(65535.f, t1) : 0.f;
+    uint32_t lo[NSUP], hi[NSUP];  // bytes of column g's weights of the tile's rows 2t, 2t + 1, 8 + 2t, 8 + 2t + 1
+#pragma unroll
+    for (int sp = 0; sp < NSUP; sp++) {
+      const uint32_t n0 = __float_as_uint(fmaf(y[sp][0], i0, MAGIC_F)), n1 = __float_as_uint(fmaf(y[sp][1], i1, MAGIC_F));
+      const uint32_t n2 = __float_as_uint(fmaf(y[sp][2], i0, MAGIC_F)), n3 = __float_as_uint(fmaf(y[sp][3], i1, MAGIC_F));
+      const uint32_t x0 = transpose8(__byte_perm(n0, n1, 0x5410)), x1 = transpose8(__byte_perm(n2, n3, 0x5410));
+      lo[sp] = __byte_perm(x0, x1, 0x6420);
+      hi[sp] = __byte_perm(x0, x1, 0x7531);
+    }
+    const int start[4] = {MAGIC, MAGIC, MAGIC, MAGIC};
+    int ah[4][4], al[4][4];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {  // two 16-key tiles a product
+      uint32_t T[2][4];  // byte c of the four keys: channels 8g + 2c (low) and 8g + 2c + 1 (high)
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        uint32_t v[4];
+        v_words(blk, p, 2 * j + k, v);
+        const uint32_t a01 = __byte_perm(v[0], v[1], 0x5140), b01 = __byte_perm(v[0], v[1], 0x7362);
+        const uint32_t a23 = __byte_perm(v[2], v[3], 0x5140), b23 = __byte_perm(v[2], v[3], 0x7362);
+        T[k][0] = __byte_perm(a01, a23, 0x5410);
+        T[k][1] = __byte_perm(a01, a23, 0x7632);
+        T[k][2] = __byte_perm(b01, b23, 0x5410);
+        T[k][3] = __byte_perm(b01, b23, 0x7632);
+      }
+      const int s0 = 2 * j / NTI, s1 = (2 * j + 1) / NTI, u0 = 2 * j % NTI, u1 = (2 * j + 1) % NTI;
+      const uint32_t h0 = in_tile(hi[s0], u0), h1 = in_tile(hi[s1], u1);
+      const uint32_t l0 = in_tile(lo[s0], u0), l1 = in_tile(lo[s1], u1);
+#pragma unroll
+      for (int mt = 0; mt < 4; mt++) {
+        const uint32_t f[4] = {T[0][mt] & 0x0f0f0f0fu, (T[0][mt] >> 4) & 0x0f0f0f0fu, T[1][mt] & 0x0f0f0f0fu,
+                               (T[1][mt] >> 4) & 0x0f0f0f0fu};
+        mma16832<false>(ah[mt], f, h0, h1, j == 0 ? start : ah[mt]);
+        mma16832<false>(al[mt], f, l0, l1, j == 0 ? start : al[mt]);
+      }
+    }
+    const float e0 = t0 * (1.f / 65535.f), e1 = t1 * (1.f / 65535.f);
+#pragma unroll
+    for (int mt = 0; mt < 4; mt++)
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        const float v = fmaf(256.f, __int_as_float(ah[mt][c]) - MAGIC_F, __int_as_float(al[mt][c]) - MAGIC_F);
+        o[p][mt][c] = fmaf(c & 1 ? e1 : e0, v, o[p][mt][c]);
+      }
+  }
+
+  // the same with float32 weights in three bf16 terms; o holds channels 8g + mt and 8g + 4 + mt
+  __device__ __forceinline__ void out_float(const uint8_t *blk, int p, int my_key, const float (*x)[4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    float ob[4][4];  // the block's own sums, added in 32-bit rounding to nearest
+#pragma unroll
+    for (int mt = 0; mt < 4; mt++)
+#pragma unroll
+      for (int c = 0; c < 4; c++) ob[mt][c] = 0.f;
+#pragma unroll
+    for (int sp = 0; sp < NSUP; sp++) {
+      const uint8_t *vp = blk + 2 * NG * PLANE + (NG + p) * PAIRS + (sp * NTI * 16 + my_key) * 4;
+      const float2 s0 = pair_at(vp), s1 = pair_at(vp + 8 * 4);
+      const float z0 = fmaf(8.f, s0.x, s0.y), z1 = fmaf(8.f, s1.x, s1.y);
+      ofs[p][0] = fmaf(x[sp][0], z0, fmaf(x[sp][2], z1, ofs[p][0]));
+      ofs[p][1] = fmaf(x[sp][1], z0, fmaf(x[sp][3], z1, ofs[p][1]));
+      uint32_t bq[3][2];  // weights as B fragments: column g, keys perm(2t), perm(2t + 1) (+ 8)
+      float y0 = x[sp][0] * s0.x, y1 = x[sp][1] * s0.x, y2 = x[sp][2] * s1.x, y3 = x[sp][3] * s1.x;
+#pragma unroll
+      for (int k = 0; k < 3; k++) {
+        const uint32_t h0 = bf2_pack_rn(y0, y1), h1 = bf2_pack_rn(y2, y3);
+        bq[k][0] = transpose8(h0);
+        bq[k][1] = transpose8(h1);
+        y0 -= __uint_as_float(h0 << 16);
+        y1 -= __uint_as_float(h0 & 0xffff0000u);
+        y2 -= __uint_as_float(h1 << 16);
+        y3 -= __uint_as_float(h1 & 0xffff0000u);
+      }
+#pragma unroll
+      for (int ti = 0; ti < NTI; ti++) {
+        uint32_t v[4];
+        v_words(blk, p, sp * NTI + ti, v);
+        const uint32_t lo01 = __byte_perm(v[0], v[1], 0x5410), hi01 = __byte_perm(v[0], v[1], 0x7632);
+        const uint32_t lo23 = __byte_perm(v[2], v[3], 0x5410), hi23 = __byte_perm(v[2], v[3], 0x7632);
+        const bool on = GP == 8 || g / GP == ti;
+        auto tile = [&](auto mtag) {
+          constexpr int mt = decltype(mtag)::value;
+          const uint32_t f[4] = {codes2<mt>(lo01), codes2<mt>(hi01), codes2<mt>(lo23), codes2<mt>(hi23)};
+#pragma unroll
+          for (int k = 2; k >= 0; k--) mma16816(ob[mt], f, on ? bq[k][0] : 0u, on ? bq[k][1] : 0u);
+        };
+        tile(std::integral_constant<int, 0>());
+        tile(std::integral_constant<int, 1>());
+        tile(std::integral_constant<int, 2>());
+        tile(std::integral_constant<int, 3>());
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 4; mt++)
+#pragma unroll
+      for (int c = 0; c < 4; c++) o[p][mt][c] += ob[mt][c];
   }
 
   // Join the lanes' sums and the key tiles' columns: afterwards the lanes with 2 t < GP hold, for
@@ -595,6 +701,8 @@ struct WarpAttn {
   }
   // four consecutive channels p * 64 + 8 g + 4 hf .. of query head 2 t + c (after join)
   __device__ __forceinline__ float4 value(int p, int hf, int c) const {
+    if constexpr (INT)
+      return make_float4(o[p][2 * hf][c], o[p][2 * hf][c + 2], o[p][2 * hf + 1][c], o[p][2 * hf + 1][c + 2]);
     return make_float4(o[p][0][c + 2 * hf], o[p][1][c + 2 * hf], o[p][2][c + 2 * hf], o[p][3][c + 2 * hf]);
   }
 };
@@ -830,101 +938,86 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
     }
     sum = __shfl_sync(0xffffffffu, incl, 31);
   }
-  // the run as segments of one item each: (b, item of the sequence, block), walked twice, by the
-  // issue of copies and, up to ST blocks behind it, by the arithmetic
-  struct Walk {
-    int b, nkeys, nb, it, blk;
-  };
-  auto enter = [&](Walk &k) {  // the first sequence from k.b on with a key
-    for (;;) {
-      k.nkeys = keys_of(a, k.b, false);
-      k.nb = (k.nkeys + KV4_BLOCK - 1) / KV4_BLOCK;
-      if (k.nb > 0) return;
-      k.b++;
+  // the run, walked twice: by the issue of copies and, up to ST blocks behind it, by the arithmetic
+  const int cap_blk = a.cap / KV4_BLOCK;
+  auto blocks_from = [&](int &sq) {  // blocks of the first sequence from sq on that has a key
+    for (;; sq++) {
+      const int nb = (keys_of(a, sq, false) + KV4_BLOCK - 1) / KV4_BLOCK;
+      if (nb > 0) return nb;
     }
   };
-  auto src = [&](const Walk &k) {
-    return a.data + ((long)(k.b * a.Hkv + k.it / a.qchunks) * (a.cap / KV4_BLOCK) + k.blk) * BLK;
-  };
-  Walk c;
-  c.b = b;
-  enter(c);
-  c.it = (f0 - before) / c.nb;
-  c.blk = (f0 - before) % c.nb;
-  Walk ld = c;
+  int nb = blocks_from(b);
+  int it = (f0 - before) / nb, blk = (f0 - before) % nb;
   Ring<BLK, ST> ring{ring_mem + warp * ST * BLK, bars + warp * ST, &s_abort, a.err};
   const int n = f1 - f0;
-  int issued = 0;
+  int issued = 0, ld_b = b, ld_it = it, ld_nb = nb, ld_left = nb - blk;
+  const uint8_t *ld = a.data + ((long)(b * a.Hkv + it / a.qchunks) * cap_blk + blk) * BLK;
   auto issue_next = [&]() {
-    if (lane == 0) ring.issue(issued, src(ld));
+    if (lane == 0) ring.issue(issued, ld);
     issued++;
-    if (issued < n && ++ld.blk == ld.nb) {
-      ld.blk = 0;
-      if (++ld.it == per_seq) {
-        ld.it = 0;
-        ld.b++;
-        enter(ld);
+    ld += BLK;
+    if (--ld_left == 0 && issued < n) {  // the next item
+      if (++ld_it == per_seq) {
+        ld_it = 0;
+        ld_b++;
+        ld_nb = blocks_from(ld_b);
       }
+      ld_left = ld_nb;
+      ld = a.data + (long)(ld_b * a.Hkv + ld_it / a.qchunks) * cap_blk * BLK;
     }
   };
   for (int i = 0; i < ST && i < n; i++) issue_next();
   W w;
-  bool fresh = true, whole = c.blk == 0;
-  for (int i = 0; i < n; i++) {
-    const int qc = c.it % a.qchunks, kvh = c.it / a.qchunks;
+  for (int i = 0; i < n;) {  // segments of one item each
+    const int kvh = it / a.qchunks, qc = it % a.qchunks;
     const int head0 = kvh * a.G + qc * GP, nq = min(GP, a.G - qc * GP);
-    if (fresh)
-      w.start(reinterpret_cast<const T *>(a.q) + (long)c.b * a.ldq + (long)head0 * D, nq, a.scale_log2);
-    fresh = false;
-    if (!ring.wait(i)) {
-      if (lane == 0) ring.drain(i, issued);
-      return;
-    }
-    w.block(ring.mem + (i % ST) * BLK, c.blk * KV4_BLOCK, c.nkeys);
-    __syncwarp();
-    if (issued < n) issue_next();  // into the stage just read
-    const bool end = c.blk + 1 == c.nb;
-    if (end || i + 1 == n) {
-      w.join();
-      if (2 * t < GP) {
-        if (whole && end) {
-          T *dst = reinterpret_cast<T *>(a.out) + (long)c.b * a.ldo + (long)head0 * D;
-#pragma unroll
-          for (int k = 0; k < 2; k++)
-            if (2 * t + k < nq) {
-              const float inv = 1.f / w.l2[k];
-#pragma unroll
-              for (int p = 0; p < NG; p++) {
-                const float4 u = w.value(p, 0, k), v = w.value(p, 1, k);
-                const float r[8] = {u.x * inv, u.y * inv, u.z * inv, u.w * inv, v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-                store8(dst + (2 * t + k) * D + p * 64 + 8 * g, r);
-              }
-            }
-        } else {
-          float *dst = a.part + (long)(gw + c.b * per_seq + c.it) * GP * (D + 4);
-#pragma unroll
-          for (int k = 0; k < 2; k++)
-            if (2 * t + k < nq) {
-              float *d = dst + (2 * t + k) * (D + 4);
-#pragma unroll
-              for (int p = 0; p < NG; p++)
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++)
-                  *reinterpret_cast<float4 *>(d + p * 64 + 8 * g + 4 * hf) = w.value(p, hf, k);
-              if (g == 0) *reinterpret_cast<float2 *>(d + D) = make_float2(w.m2[k], w.l2[k]);
-            }
-        }
+    const int nkeys = keys_of(a, b, false);
+    const int take = min(nb - blk, n - i);
+    w.start(reinterpret_cast<const T *>(a.q) + (long)b * a.ldq + (long)head0 * D, nq, a.scale_log2);
+    for (int k = 0; k < take; k++, i++) {
+      if (!ring.wait(i)) {
+        if (lane == 0) ring.drain(i, issued);
+        return;
       }
-      fresh = true;
-      whole = true;
+      w.block(ring.mem + (i % ST) * BLK, (blk + k) * KV4_BLOCK, nkeys);
+      __syncwarp();
+      if (issued < n) issue_next();  // into the stage just read
     }
-    if (i + 1 < n && ++c.blk == c.nb) {
-      c.blk = 0;
-      if (++c.it == per_seq) {
-        c.it = 0;
-        c.b++;
-        enter(c);
+    w.join();
+    if (2 * t < GP) {
+      if (take == nb) {
+        T *dst = reinterpret_cast<T *>(a.out) + (long)b * a.ldo + (long)head0 * D;
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+          if (2 * t + k < nq) {
+            const float inv = 1.f / w.l2[k];
+#pragma unroll
+            for (int p = 0; p < NG; p++) {
+              const float4 u = w.value(p, 0, k), v = w.value(p, 1, k);
+              const float r[8] = {u.x * inv, u.y * inv, u.z * inv, u.w * inv, v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+              store8(dst + (2 * t + k) * D + p * 64 + 8 * g, r);
+            }
+          }
+      } else {
+        float *dst = a.part + (long)(gw + b * per_seq + it) * GP * (D + 4);
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+          if (2 * t + k < nq) {
+            float *d = dst + (2 * t + k) * (D + 4);
+#pragma unroll
+            for (int p = 0; p < NG; p++)
+#pragma unroll
+              for (int hf = 0; hf < 2; hf++)
+                *reinterpret_cast<float4 *>(d + p * 64 + 8 * g + 4 * hf) = w.value(p, hf, k);
+            if (g == 0) *reinterpret_cast<float2 *>(d + D) = make_float2(w.m2[k], w.l2[k]);
+          }
       }
+    }
+    blk = 0;
+    if (i < n && ++it == per_seq) {
+      it = 0;
+      b++;
+      nb = blocks_from(b);
     }
   }
 }

@@ -67,14 +67,16 @@ def attend(data, d, q, lens, scale, out_eps):
     The tolerance counts, per element, with unit roundoffs u = 2^-23 (float32, either rounding
     mode) and out_eps (half a step of the output type):
       out_eps |o|                       the stored output
-      out_eps sum_j w_j s_j |c_j - 8|   the weights w_j s_j as they enter the output product (for
-                                        float32 three bf16 terms: 2^-24)
+      out_eps sum_j w_j s_j |c_j - 8|   float32: the weights w_j s_j as they enter the output product in
+                                        three bf16 terms (2^-24)
       2 E sum_j w_j |v_j|               scores off by E = (d + 8) u scale (sum |q||s (c - 8)| +
                                         |m + 8 s| sum |q|) at most over the keys, times log 2 rounding
                                         and the exponential (2^-21), on weights and on their sum
       n u sum_j w_j |v_j|               the sums over n keys, of weights and of products
     bfloat16 (out_eps 2^-8) scores are taken with q in steps of its plane's largest |q| / 32512: each
     q is off by half a step at most, so E has scale sum over planes of (half a step) sum s c more.
+    Its weights w_j s_j are taken in steps of the largest of a block of 64 keys / 65535: sum over
+    blocks of half a step times sum c.
     """
     codes, s, m = unpack(data, d)
     B, Hq, _ = q.shape
@@ -104,5 +106,13 @@ def attend(data, d, q, lens, scale, out_eps):
             absv = w @ np.abs(v) + w @ (np.abs(vm + 8 * vs)[..., None] + np.zeros((1, 1, 64))).reshape(n, d)
             spread = w @ (np.abs(vc - 8) * vs[..., None]).reshape(n, d)
             out[b, h] = o
-            tol[b, h] = out_eps * np.abs(o) + out_eps * spread + (2 * E + (n + 16) * u) * absv
+            if out_eps == 2.0 ** -8:
+                spread = np.zeros(d)
+                for j in range(0, n, 64):
+                    step = (w[j:j + 64, None] * vs[j:j + 64]).max(0) / 65535         # [ng]
+                    spread += (step[:, None] / 2 * vc[j:j + 64].sum(0)).reshape(d)
+                tol[b, h] = out_eps * np.abs(o) + spread
+            else:
+                tol[b, h] = out_eps * np.abs(o) + out_eps * spread
+            tol[b, h] += (2 * E + (n + 16) * u) * absv
     return out, tol
