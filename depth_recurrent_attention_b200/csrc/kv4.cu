@@ -883,7 +883,8 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
 // sequence, item by item, and every warp of a grid that fills the GPU once takes an equal run of it,
 // whatever the lengths.  A warp that holds a whole item writes its output; the others leave
 // partial outputs in slot (warp + item), and kv4_join_kernel joins an item's slots, which are
-// consecutive.
+// consecutive.  Where all of a CTA's runs lie in one item, its warps join first and leave one slot,
+// that of the first warp.
 __device__ __forceinline__ int warp_incl_sum(int v) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -906,6 +907,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
   extern __shared__ __align__(128) uint8_t ring_mem[];
   __shared__ __align__(8) uint64_t bars[NW * ST];
   __shared__ int s_abort;
+  __shared__ int s_one;  // item + 1 where the CTA's runs lie in one item and leave one slot, else 0
+  __shared__ float sm_m[NW][GP], sm_l[NW][GP];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -914,6 +917,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
     for (int i = 0; i < NW * ST; i++) tc::mbar_init(tc::smem_u32(&bars[i]), 1);
     tc::fence_mbar_init();
     s_abort = 0;
+    s_one = 0;
   }
   if (blockIdx.x == 0 && warp == 0)
     for (int i = lane; i < a.B; i += 32) keys_of(a, i, true);
@@ -923,7 +927,10 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
   const int total = total_blocks(a, per_seq);
   const int per = (total + a.n_warps - 1) / a.n_warps;
   const int f0 = min((long)gw * per, (long)total), f1 = min((long)f0 + per, (long)total);
-  if (f0 >= f1) return;
+  const long c0 = (long)blockIdx.x * NW * per, c1 = min(c0 + (long)NW * per, (long)total);  // of the CTA
+  if (c0 >= c1) return;  // the whole CTA
+  bool one = false;
+  if (f0 < f1) {
   // the sequence of block f0, and the blocks before it
   int b = 0, before = 0;
   for (int i0 = 0, sum = 0; i0 < a.B; i0 += 32) {
@@ -948,6 +955,10 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
   };
   int nb = blocks_from(b);
   int it = (f0 - before) / nb, blk = (f0 - before) % nb;
+  {
+    const int i0 = before + it * nb;  // the item of the warp's first block
+    one = i0 <= c0 && c1 <= i0 + nb && per < nb;
+  }
   Ring<BLK, ST> ring{ring_mem + warp * ST * BLK, bars + warp * ST, &s_abort, a.err};
   const int n = f1 - f0;
   int issued = 0, ld_b = b, ld_it = it, ld_nb = nb, ld_left = nb - blk;
@@ -977,7 +988,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
     for (int k = 0; k < take; k++, i++) {
       if (!ring.wait(i)) {
         if (lane == 0) ring.drain(i, issued);
-        return;
+        i = n;
+        break;
       }
       w.block(ring.mem + (i % ST) * BLK, (blk + k) * KV4_BLOCK, nkeys);
       __syncwarp();
@@ -985,7 +997,22 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
     }
     w.join();
     if (2 * t < GP) {
-      if (take == nb) {
+      if (one) {  // into the warp's own stages, all read
+        float *dst = reinterpret_cast<float *>(ring.mem);
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          if (g == 0) {
+            sm_m[warp][2 * t + k] = w.m2[k];
+            sm_l[warp][2 * t + k] = w.l2[k];
+          }
+#pragma unroll
+          for (int p = 0; p < NG; p++)
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++)
+              *reinterpret_cast<float4 *>(dst + (2 * t + k) * D + p * 64 + 8 * g + 4 * hf) = w.value(p, hf, k);
+        }
+        if (warp == 0 && lane == 0) s_one = b * per_seq + it + 1;
+      } else if (take == nb) {
         T *dst = reinterpret_cast<T *>(a.out) + (long)b * a.ldo + (long)head0 * D;
 #pragma unroll
         for (int k = 0; k < 2; k++)
@@ -1020,20 +1047,49 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
       nb = blocks_from(b);
     }
   }
+  } else if (warp > 0 && lane < GP) {  // no blocks: nothing to add to the CTA's item
+    sm_m[warp][lane] = -INFINITY;
+    sm_l[warp][lane] = 0.f;
+  }
+  __syncthreads();
+  if (s_one == 0) return;
+  // one slot of the CTA
+  float *dst = a.part + (long)(blockIdx.x * NW + s_one - 1) * GP * (D + 4);
+  static_assert(GP * D * 4 <= ST * BLK, "a warp's stages hold its partial output");
+  for (int e = threadIdx.x; e < GP * D; e += NW * 32) {
+    const int qh = e / D;
+    float m = sm_m[0][qh];
+#pragma unroll
+    for (int k = 1; k < NW; k++) m = fmaxf(m, sm_m[k][qh]);
+    float acc = 0.f, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; k++) {
+      const bool none = c0 + k * (long)per >= c1;  // a warp without blocks
+      const float f = none ? 0.f : sm_m[k][qh] == -INFINITY ? 1.f : tc::ex2(sm_m[k][qh] - m);
+      if (!none) acc = fmaf(f, reinterpret_cast<const float *>(ring_mem + k * ST * BLK)[e], acc);
+      l = fmaf(f, sm_l[k][qh], l);
+    }
+    dst[qh * (D + 4) + e % D] = acc;
+    if (e % D == 0) *reinterpret_cast<float2 *>(dst + qh * (D + 4) + D) = make_float2(m, l);
+  }
 }
 
-// Join the slots of an item's query head: eight warps take every eighth slot, a lane D / 32
-// channels, then the warps join in shared memory.  Items that one warp held are done; items without
-// a key get zeros.
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a) {
+// Join the slots of an item's query head: `share` warps of a CTA (1 to 8) take turns at its slots, a
+// lane D / 32 channels, then join in shared memory.  An item's slots are those of the warps that hold a
+// part of it, one a CTA where the whole CTA does.  Items that one warp held are done; items without a
+// key get zeros.
+template <typename T, int D, int GP, int SNW>
+__global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a, int share) {
   constexpr int NW = 8, C = D / 32;
   __shared__ float so[NW][D], sm[NW], sl[NW];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_seq = a.Hkv * a.qchunks;
-  const int b = blockIdx.x / (a.Hkv * a.G), head = blockIdx.x % (a.Hkv * a.G);
+  const int per_seq = a.Hkv * a.qchunks, Hq = a.Hkv * a.G;
+  const int part_of = warp % share;  // this warp's turn
+  const long out = (long)blockIdx.x * (NW / share) + warp / share;
+  const bool live = out < (long)a.B * Hq;
+  const int b = live ? (int)(out / Hq) : 0, head = live ? (int)(out % Hq) : 0;
   const int kvh = head / a.G, qh = head % a.G;
   const int it = kvh * a.qchunks + qh / GP;
   int sum = 0, upto = 0;  // blocks of all sequences, and of those before b
@@ -1045,79 +1101,93 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a) {
   sum = __reduce_add_sync(0xffffffffu, sum) * per_seq;
   upto = __reduce_add_sync(0xffffffffu, upto) * per_seq;
   const int nb = (keys_of(a, b, false) + KV4_BLOCK - 1) / KV4_BLOCK;
-  T *dst = reinterpret_cast<T *>(a.out) + (long)b * a.ldo + (long)head * D;
-  if (nb == 0) {
-    for (int e = threadIdx.x; e < D; e += 256) dst[e] = from_f<T>(0.f);
-    return;
-  }
   const int per = (sum + a.n_warps - 1) / a.n_warps;
-  const int s = upto + it * nb;
-  const int w0 = s / per, w1 = (s + nb - 1) / per;
-  if (w0 == w1) return;
-  const float *part = a.part + ((long)(w0 + b * per_seq + it) * GP + qh % GP) * (D + 4);
-  const long step = (long)GP * (D + 4);
-  const int n = w1 - w0 + 1;
+  const int s = upto + it * nb;  // blocks s .. s + nb - 1
+  const int w0 = nb ? s / per : 0, w1 = nb ? (s + nb - 1) / per : 0;
   float m = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; c++) acc[c] = 0.f;
-  // four slots a step, their loads in flight together
-  for (int i = warp; i < n; i += 4 * NW) {
-    float2 ml[4];
-    float v[4][C];
+  const bool held = w0 == w1;  // by one warp (or no block at all)
+  if (live && !held) {
+    // the CTAs cA .. cB hold the item: one slot each, but the first and the last a slot a warp where
+    // they hold another item too
+    auto joined = [&](int c) {  // as in the split kernel
+      const long c0 = (long)c * SNW * per, c1 = min(c0 + (long)SNW * per, (long)sum);
+      return s <= c0 && c1 <= s + nb && per < nb;
+    };
+    const int cA = w0 / SNW, cB = w1 / SNW;
+    const int nA = joined(cA) ? 1 : min(w1, cA * SNW + SNW - 1) - w0 + 1;
+    const int mid = max(0, cB - cA - 1);
+    const int nB = cA == cB ? 0 : joined(cB) ? 1 : w1 - cB * SNW + 1;
+    const int n = nA + mid + nB;
+    const long step = (long)GP * (D + 4);
+    const float *base = a.part + ((long)(b * per_seq + it) * GP + qh % GP) * (D + 4);
+    auto slot = [&](int j) {
+      const int w = j < nA ? w0 + j : j < nA + mid ? (cA + 1 + j - nA) * SNW : cB * SNW + j - nA - mid;
+      return base + w * step;
+    };
+    // four slots a step, their loads in flight together
+    for (int i = part_of; i < n; i += 4 * share) {
+      float2 ml[4];
+      float v[4][C];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const int j = i + k * NW;
-      ml[k] = make_float2(-INFINITY, 0.f);
+      for (int k = 0; k < 4; k++) {
+        const int j = i + k * share;
+        ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int c = 0; c < C; c++) v[k][c] = 0.f;
-      if (j < n) {
-        const float *p = part + j * step;
-        ml[k] = *reinterpret_cast<const float2 *>(p + D);
-        if constexpr (C == 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(p + 4 * lane);
-          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2 *>(p + 2 * lane);
-          v[k][0] = x.x; v[k][1] = x.y;
+        for (int c = 0; c < C; c++) v[k][c] = 0.f;
+        if (j < n) {
+          const float *p = slot(j);
+          ml[k] = *reinterpret_cast<const float2 *>(p + D);
+          if constexpr (C == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + 4 * lane);
+            v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2 *>(p + 2 * lane);
+            v[k][0] = x.x; v[k][1] = x.y;
+          }
         }
       }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < 4; k++) mn = fmaxf(mn, ml[k].x);
+      const float al = m == -INFINITY ? 1.f : tc::ex2(m - mn);
+      l *= al;
+#pragma unroll
+      for (int c = 0; c < C; c++) acc[c] *= al;
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float f = ml[k].x == -INFINITY ? 1.f : tc::ex2(ml[k].x - mn);
+        l = fmaf(f, ml[k].y, l);
+#pragma unroll
+        for (int c = 0; c < C; c++) acc[c] = fmaf(f, v[k][c], acc[c]);
+      }
+      m = mn;
     }
-    float mn = m;
+  }
+  if (share > 1) {
 #pragma unroll
-    for (int k = 0; k < 4; k++) mn = fmaxf(mn, ml[k].x);
-    const float al = m == -INFINITY ? 1.f : tc::ex2(m - mn);
-    l *= al;
-#pragma unroll
-    for (int c = 0; c < C; c++) acc[c] *= al;
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const float f = ml[k].x == -INFINITY ? 1.f : tc::ex2(ml[k].x - mn);
-      l = fmaf(f, ml[k].y, l);
-#pragma unroll
-      for (int c = 0; c < C; c++) acc[c] = fmaf(f, v[k][c], acc[c]);
+    for (int c = 0; c < C; c++) so[warp][C * lane + c] = acc[c];
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
     }
-    m = mn;
-  }
+    __syncthreads();
+    if (part_of) return;
+    for (int k = warp + 1; k < warp + share; k++) {
+      const float mn = fmaxf(m, sm[k]);
+      const float f0 = m == -INFINITY ? 1.f : tc::ex2(m - mn), f1 = sm[k] == -INFINITY ? 1.f : tc::ex2(sm[k] - mn);
+      l = fmaf(f1, sl[k], l * f0);
 #pragma unroll
-  for (int c = 0; c < C; c++) so[warp][C * lane + c] = acc[c];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < D; e += 256) {
-    float M = sm[0];
-#pragma unroll
-    for (int k = 1; k < NW; k++) M = fmaxf(M, sm[k]);
-    float r = 0.f, L = 0.f;
-#pragma unroll
-    for (int k = 0; k < NW; k++) {
-      const float f = sm[k] == -INFINITY ? 1.f : tc::ex2(sm[k] - M);
-      r = fmaf(f, so[k][e], r);
-      L = fmaf(f, sl[k], L);
+      for (int c = 0; c < C; c++) acc[c] = fmaf(f1, so[k][C * lane + c], acc[c] * f0);
+      m = mn;
     }
-    dst[e] = from_f<T>(r / L);
   }
+  if (!live || (held && nb)) return;
+  T *dst = reinterpret_cast<T *>(a.out) + (long)b * a.ldo + (long)head * D;
+  const float inv = nb ? 1.f / l : 0.f;
+#pragma unroll
+  for (int c = 0; c < C; c++) dst[C * lane + c] = from_f<T>(nb ? acc[c] * inv : 0.f);
 }
 
 template <typename K, typename... A>
@@ -1200,7 +1270,11 @@ int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
     if (rc) return rc;
     LaunchOpt j;
     j.pdl = true;  // the split kernel precedes it on the stream
-    return launch(kv4_join_kernel<T, W::D, GP>, dim3((unsigned)(a.B * a.Hkv * a.G)), dim3(256), 0, 1, s, j, a);
+    // warps a query head: one for each four of the slots that items have on average
+    const long outs = (long)a.B * a.Hkv * a.G, mean = a.n_warps / items;
+    const int share = mean > 64 ? 8 : mean > 32 ? 4 : mean > 8 ? 2 : 1;
+    return launch(kv4_join_kernel<T, W::D, GP, C::NW>, dim3((unsigned)((outs * share + 7) / 8)), dim3(256), 0, 1, s, j, a,
+                  share);
   }
   constexpr int NW = 4, ST = 3;
   // CTAs of an item: at least a block a warp, and no more than fill the GPU
