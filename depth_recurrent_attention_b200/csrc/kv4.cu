@@ -31,11 +31,11 @@ constexpr int PLANE = KV4_BLOCK * 32;  // bytes of a code plane of a block
 constexpr int PAIRS = KV4_BLOCK * 4;   // bytes of a pair plane of a block
 
 // ---- rows in and out -------------------------------------------------------------------
-// A CTA takes ROWS_T rows and eight (head, plane) pairs of the keys or of the values
-// (blockIdx.z), a warp one of the eight: 8 lanes hold a group's 64 channels, so a warp step is
-// four consecutive rows of one (head, plane): 128-byte reads, and 128 contiguous bytes of codes
-// and 16 of pairs where the rows are neighbours in a block.
-constexpr int ROWS_T = 16;
+// A CTA takes ROWS rows and eight (head, plane) pairs of the keys or of the values (blockIdx.z), a
+// warp one of the eight: 8 lanes hold a group's 64 channels, so a warp step is four consecutive
+// rows of one (head, plane), 128-byte reads, and 128 contiguous bytes of codes and 16 of pairs
+// where the rows are neighbours in a block; four steps are in flight at a time.  64 rows a CTA where
+// that still fills the GPU (the search for the rows' places is paid once a CTA), else 16.
 constexpr int CU_SMEM = 1024;  // boundaries searched in shared memory up to this many sequences
 
 struct RowArgs {
@@ -49,9 +49,10 @@ struct RowArgs {
   int *err;
 };
 
-// Block offset (in blocks, of head 0) and position in the block of the tile's rows: row r
-// belongs to the sequence b with cu[b] <= r < cu[b + 1].  slot < 0: the row is in no sequence,
-// or its position is outside the cache (reported).
+// Block (of head 0) and position in the sequence of the CTA's rows: row r belongs to the sequence b
+// with cu[b] <= r < cu[b + 1].  A position below 0: the row is in no sequence, or its place is outside
+// the cache (reported).
+template <int ROWS>
 __device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu, long *blk, int *pos) {
   const int tid = threadIdx.x;
   const int *cu = a.cu;
@@ -60,7 +61,7 @@ __device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu,
     cu = scu;
   }
   __syncthreads();
-  if (tid < ROWS_T) {
+  if (tid < ROWS) {
     const int r = row0 + tid;
     int p = -1, b = -1, off = 0;
     if (r < a.n_rows) {
@@ -90,85 +91,190 @@ __device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu,
   __syncthreads();
 }
 
+// Eight consecutive values as they were read
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float *p) { load8(p, v); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = 0.f;
+  }
+  // the largest value and the largest negated value of the group's 8 lanes; NaN where one is
+  __device__ __forceinline__ void range(float &mx, float &neg) const {
+    mx = v[0];
+    neg = -v[0];
+#pragma unroll
+    for (int e = 1; e < 8; e++) {
+      mx = max_nan(mx, v[e]);
+      neg = max_nan(neg, -v[e]);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      neg = max_nan(neg, __shfl_xor_sync(0xffffffffu, neg, o));
+    }
+  }
+  static __device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  }
+  __device__ __forceinline__ float value(int e) const { return v[e]; }
+  __device__ __forceinline__ float minus(int e, float m) const { return v[e] - m; }
+};
+template <> struct Raw8<bf16> {
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const bf16 *p) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
+  }
+  __device__ __forceinline__ void zero() { u[0] = u[1] = u[2] = u[3] = 0; }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ __forceinline__ void range(float &mx, float &neg) const {
+    const uint32_t sign = 0x80008000u;
+    const uint32_t hi = max2(max2(u[0], u[1]), max2(u[2], u[3]));
+    const uint32_t lo = max2(max2(u[0] ^ sign, u[1] ^ sign), max2(u[2] ^ sign, u[3] ^ sign));
+    // (max, max of the negated) in the two halves of a word
+    uint32_t r = max2(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) r = max2(r, __shfl_xor_sync(0xffffffffu, r, o));
+    mx = __uint_as_float(r << 16);
+    neg = __uint_as_float(r & 0xffff0000u);
+  }
+  __device__ __forceinline__ float value(int e) const {
+    return __uint_as_float(e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+  }
+  // x - m rounded once, the bf16 half taken as it is
+  __device__ __forceinline__ float minus(int e, float m) const {
+    float d;
+    if (e & 1)
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tfma.rn.f32.bf16 %0, h, %2, %3;\n\t}"
+          : "=f"(d) : "r"(u[e >> 1]), "h"((unsigned short)0x3F80), "f"(-m));
+    else
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tfma.rn.f32.bf16 %0, l, %2, %3;\n\t}"
+          : "=f"(d) : "r"(u[e >> 1]), "h"((unsigned short)0x3F80), "f"(-m));
+    return d;
+  }
+};
+
+// c = min(max(rint((x - m) / s), 0), 15) of the exact quotient, the form in 64 bits
+__device__ __noinline__ float code_exact(float x, float m, float s) {
+  const double q = rint(((double)x - (double)m) / (double)s);
+  return (float)fmin(fmax(q, 0.0), 15.0);
+}
+// (max - min) / 15 in 64 bits
+__device__ __noinline__ float step_exact(float mx, float mn) { return (float)(((double)mx - (double)mn) / 15.0); }
+
+// Eight codes of a lane's values, four bits each.  The quotient in 32 bits is off by less than 2^-19,
+// so it rounds as the exact one does unless that lies within 2^-16 of a half, which the remainder
+// d - c s (exact: at most 20 bits) shows.  There the remainder decides where d = x - m is
+// exact, as it nearly always is for bfloat16 (a tie goes to the even code), else the form in 64 bits.
+// bfloat16: m is the minimum itself and s within 2^-9 of a 15th, so quotients lie in 0 .. 15.1.
 template <typename T>
+__device__ __forceinline__ uint32_t codes8(const Raw8<T> &x, float m, float s) {
+  constexpr bool CLAMP = sizeof(T) == 4;
+  const float inv = 1.0f / s, near = s * (0.5f - 0x1p-16f);
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    const float d = x.minus(e, m);
+    float n;  // 1.5 * 2^23 + the rounded quotient, half to even
+    bool in = true;
+    if (CLAMP) {
+      const float y = fminf(fmaxf(d * inv, 0.f), 15.f);
+      n = y + 12582912.f;
+      in = y > 0.f && y < 15.f;
+    } else {
+      n = fmaf(d, inv, 12582912.f);
+    }
+    const float t = fmaf(12582912.f - n, s, d);
+    if (fabsf(t) >= near && in) {
+      const float v = x.value(e), h = 0.5f * s;
+      if (d + m == v && v - d == m) {
+        const bool odd = __float_as_uint(n) & 1u;
+        if (t > h || (t == h && odd)) n += 1.f;
+        else if (t < -h || (t == -h && odd)) n -= 1.f;
+      } else {
+        n = code_exact(v, m, s) + 12582912.f;
+      }
+    }
+    w += __float_as_uint(n) << (4 * e);
+  }
+  // the sum of 0x4B400000 << 4 e
+  constexpr uint32_t base = 0x4B400000u + 0xB4000000u + 0x40000000u;
+  return w - base;
+}
+
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(256) kv4_store_kernel(RowArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ int scu[CU_SMEM + 1];
-  __shared__ long sblk[ROWS_T];
-  __shared__ int spos[ROWS_T];
-  const int row0 = blockIdx.x * ROWS_T;
-  find_slots(a, row0, scu, sblk, spos);
+  __shared__ long sblk[ROWS];
+  __shared__ int spos[ROWS];
+  const int row0 = blockIdx.x * ROWS;
+  find_slots<ROWS>(a, row0, scu, sblk, spos);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.y * 8 + warp;  // head * ng + plane
   if (hp >= a.Hkv * a.ng) return;
   const int head = hp / a.ng, plane = hp % a.ng;
   const int side = blockIdx.z;
-  const T *src = reinterpret_cast<const T *>(side ? a.v : a.k) + (long)hp * KV4_GROUP + (lane & 7) * 8;
-  const long ld = side ? a.ldv : a.ldk;
   const int sub = lane >> 3;
-  float x[ROWS_T / 4][8];
-#pragma unroll
-  for (int i = 0; i < ROWS_T / 4; i++)
-    if (spos[i * 4 + sub] >= 0) load8(src + (long)(row0 + i * 4 + sub) * ld, x[i]);
-  const long head_blk = (long)head * (a.cap / KV4_BLOCK);
+  const long ld = side ? a.ldv : a.ldk;
+  const T *src = reinterpret_cast<const T *>(side ? a.v : a.k) + (long)hp * KV4_GROUP + (lane & 7) * 8 +
+                 (long)(row0 + sub) * ld;
   const int block_bytes = a.ng * 2 * (PLANE + PAIRS);
-#pragma unroll
-  for (int i = 0; i < ROWS_T / 4; i++) {
-    const int p = spos[i * 4 + sub];
-    if (p < 0) {
-#pragma unroll
-      for (int e = 0; e < 8; e++) x[i][e] = 0.f;
-    }
-    float mx = x[i][0], mn = x[i][0], bad = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      mx = fmaxf(mx, x[i][e]);
-      mn = fminf(mn, x[i][e]);
-      if (!(fabsf(x[i][e]) <= 0x1p126f)) bad = 1.f;  // NaN, infinite or out of range
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      bad = fmaxf(bad, __shfl_xor_sync(0xffffffffu, bad, o));
-    }
-    bf16 sb = __float2bfloat16_rn((float)(((double)mx - (double)mn) / 15.0));
-    bf16 mb = __float2bfloat16_rn(mn);
-    if (bad != 0.f) sb = mb = __float2bfloat16_rn(NAN);
-    const float s = __bfloat162float(sb), m = __bfloat162float(mb);
+  uint8_t *dst = a.data + (long)head * (a.cap / KV4_BLOCK) * block_bytes + (side * a.ng + plane) * PLANE + (lane & 7) * 4;
+  // from a row's codes (of lane 0 of its 8) to its pair: + pair_at + t * (4 - 32)
+  const int pair_at = 2 * a.ng * PLANE + (side * a.ng + plane) * (PAIRS - PLANE);
+  Raw8<T> next;
+  next.zero();
+  if (spos[sub] >= 0) next.load(src);
+#pragma unroll 1
+  for (int r = 0; r < ROWS; r += 4) {
+    const Raw8<T> x = next;
+    const int p = spos[r + sub];
+    src += 4 * ld;
+    if (r + 4 < ROWS && spos[r + 4 + sub] >= 0) next.load(src);  // the next rows', in flight meanwhile
+    float mx, neg;
+    x.range(mx, neg);
+    // s = bf16((max - min) / 15): in 32 bits off by 2 steps at most, so a rounding within 4 of a tie is
+    // taken in 64
+    float sf = (mx + neg) * (1.0f / 15.0f);
+    if ((((__float_as_uint(sf) + 4u) & 0xffffu) - 0x8000u) <= 8u || sf < 0x1p-100f) sf = step_exact(mx, -neg);
+    float s = __bfloat162float(__float2bfloat16_rn(sf)), m = __bfloat162float(__float2bfloat16_rn(-neg));
+    if (!(fmaxf(mx, neg) <= 0x1p126f) || !(mx + neg >= 0.f)) s = m = NAN;  // NaN, infinite, out of range
     uint32_t w = 0;
-    if (s > 0.f) {
+    if (s >= 0x1p-100f) {
+      w = codes8<T>(x, m, s);
+    } else if (s > 0.f) {
 #pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const double qd = ((double)x[i][e] - (double)m) / (double)s;
-        const int c = (int)fmin(fmax(rint(qd), 0.0), 15.0);
-        w |= (uint32_t)c << (4 * e);
-      }
+      for (int e = 0; e < 8; e++) w |= (uint32_t)code_exact(x.value(e), m, s) << (4 * e);
     }
     if (p >= 0) {
-      uint8_t *blk = a.data + (sblk[i * 4 + sub] + head_blk) * block_bytes;
       const int t = p % KV4_BLOCK;
-      *reinterpret_cast<uint32_t *>(blk + (side * a.ng + plane) * PLANE + t * 32 + (lane & 7) * 4) = w;
-      if ((lane & 7) == 0) {
-        __nv_bfloat162 pr;
-        pr.x = sb;
-        pr.y = mb;
-        *reinterpret_cast<__nv_bfloat162 *>(blk + 2 * a.ng * PLANE + (side * a.ng + plane) * PAIRS + t * 4) = pr;
-      }
+      uint8_t *q = dst + sblk[r + sub] * block_bytes + t * 32;
+      *reinterpret_cast<uint32_t *>(q) = w;
+      if ((lane & 7) == 0)
+        *reinterpret_cast<uint32_t *>(q + pair_at - t * 28) = bf2_pack_rn(s, m);
     }
   }
 }
 
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ int scu[CU_SMEM + 1];
-  __shared__ long sblk[ROWS_T];
-  __shared__ int spos[ROWS_T];
-  const int row0 = blockIdx.x * ROWS_T;
-  find_slots(a, row0, scu, sblk, spos);
+  __shared__ long sblk[ROWS];
+  __shared__ int spos[ROWS];
+  const int row0 = blockIdx.x * ROWS;
+  find_slots<ROWS>(a, row0, scu, sblk, spos);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.y * 8 + warp;
   if (hp >= a.Hkv * a.ng) return;
@@ -179,27 +285,30 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
   const int sub = lane >> 3;
   const long head_blk = (long)head * (a.cap / KV4_BLOCK);
   const int block_bytes = a.ng * 2 * (PLANE + PAIRS);
-  uint32_t w[ROWS_T / 4];
-  float2 sm[ROWS_T / 4];
+#pragma unroll 1
+  for (int r0 = 0; r0 < ROWS; r0 += 16) {
+    uint32_t w[4], pr[4];
+    int p[4];
 #pragma unroll
-  for (int i = 0; i < ROWS_T / 4; i++) {
-    const int p = spos[i * 4 + sub];
-    w[i] = 0;
-    sm[i] = make_float2(0.f, 0.f);
-    if (p < 0) continue;
-    const uint8_t *blk = a.data + (sblk[i * 4 + sub] + head_blk) * block_bytes;
-    const int t = p % KV4_BLOCK;
-    w[i] = *reinterpret_cast<const uint32_t *>(blk + (side * a.ng + plane) * PLANE + t * 32 + (lane & 7) * 4);
-    sm[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(
-        blk + 2 * a.ng * PLANE + (side * a.ng + plane) * PAIRS + t * 4));
-  }
+    for (int i = 0; i < 4; i++) {
+      p[i] = spos[r0 + i * 4 + sub];
+      w[i] = pr[i] = 0;
+      if (p[i] < 0) continue;
+      const uint8_t *blk = a.data + (sblk[r0 + i * 4 + sub] + head_blk) * block_bytes;
+      const int t = p[i] % KV4_BLOCK;
+      w[i] = *reinterpret_cast<const uint32_t *>(blk + (side * a.ng + plane) * PLANE + t * 32 + (lane & 7) * 4);
+      pr[i] = *reinterpret_cast<const uint32_t *>(blk + 2 * a.ng * PLANE + (side * a.ng + plane) * PAIRS + t * 4);
+    }
 #pragma unroll
-  for (int i = 0; i < ROWS_T / 4; i++) {
-    if (spos[i * 4 + sub] < 0 && !(a.zero_rest && row0 + i * 4 + sub < a.n_rows)) continue;
-    float x[8];
+    for (int i = 0; i < 4; i++) {
+      const int r = row0 + r0 + i * 4 + sub;
+      if (p[i] < 0 && !(a.zero_rest && r < a.n_rows)) continue;
+      const float s = __uint_as_float(pr[i] << 16), m = __uint_as_float(pr[i] & 0xffff0000u);
+      float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; e++) x[e] = fmaf(sm[i].x, (float)((w[i] >> (4 * e)) & 15u), sm[i].y);
-    store8(dst + (long)(row0 + i * 4 + sub) * ld, x);
+      for (int e = 0; e < 8; e++) x[e] = fmaf(s, (float)((w[i] >> (4 * e)) & 15u), m);
+      store8(dst + (long)r * ld, x);
+    }
   }
 }
 
@@ -209,7 +318,8 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
 //   scores   A = 16 keys x channels of K codes, B = channels x 8 columns of q
 //   output   A = 16 channels x 16 keys of V codes, B = keys x 8 columns of weights
 // What bounds it is turning nibbles into operands (the integer pipe), so
-//   - bfloat16 runs on 8-bit integer products (m16n8k32): a mask and a shift make four codes a word.
+//   - bfloat16 runs on 8-bit integer products (m16n8k32): one mask makes four codes a word (the high
+//     halves of bytes enter as 16 c).
 //     q enters as a 16-bit fixed-point number of its plane's largest |q|, in two signed bytes, a weight
 //     p s as one of its column's largest in the block, in two unsigned bytes; the integer sums are
 //     exact.  Both are finer than the bf16 rounding of q, and of the output (2^-16 and 2^-17 of the
@@ -398,24 +508,26 @@ struct WarpAttn {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint8_t *kr = blk + p * PLANE + (sp * NTI * 16 + perm_row(g)) * 32 + 8 * t;
     if constexpr (INT) {
+      // even channels (c) and odd ones (16 c: the high half of a byte as it lies) in sums of their own
       const int start[4] = {MAGIC, MAGIC, MAGIC, MAGIC};
-      int hi[4], lo[4];
+      int he[4], le[4], ho[4], lo[4];
 #pragma unroll
       for (int ti = 0; ti < NTI; ti++) {
         const uint2 w0 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32);
         const uint2 w1 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32 + 8 * 32);
-        const uint32_t ww0[2] = {w0.x, w0.y}, ww1[2] = {w1.x, w1.y};
-#pragma unroll
-        for (int w = 0; w < 2; w++) {
-          const uint32_t a[4] = {ww0[w] & 0x0f0f0f0fu, ww1[w] & 0x0f0f0f0fu, (ww0[w] >> 4) & 0x0f0f0f0fu,
-                                 (ww1[w] >> 4) & 0x0f0f0f0fu};
-          mma16832<true>(hi, a, in_tile(qf[p][4 * w], ti), in_tile(qf[p][4 * w + 2], ti), ti + w == 0 ? start : hi);
-          mma16832<true>(lo, a, in_tile(qf[p][4 * w + 1], ti), in_tile(qf[p][4 * w + 3], ti), ti + w == 0 ? start : lo);
-        }
+        const uint32_t ev[4] = {w0.x & 0x0f0f0f0fu, w1.x & 0x0f0f0f0fu, w0.y & 0x0f0f0f0fu, w1.y & 0x0f0f0f0fu};
+        const uint32_t od[4] = {w0.x & 0xf0f0f0f0u, w1.x & 0xf0f0f0f0u, w0.y & 0xf0f0f0f0u, w1.y & 0xf0f0f0f0u};
+        mma16832<true>(he, ev, in_tile(qf[p][0], ti), in_tile(qf[p][4], ti), ti == 0 ? start : he);
+        mma16832<true>(le, ev, in_tile(qf[p][1], ti), in_tile(qf[p][5], ti), ti == 0 ? start : le);
+        mma16832<true>(ho, od, in_tile(qf[p][2], ti), in_tile(qf[p][6], ti), ti == 0 ? start : ho);
+        mma16832<true>(lo, od, in_tile(qf[p][3], ti), in_tile(qf[p][7], ti), ti == 0 ? start : lo);
       }
 #pragma unroll
-      for (int c = 0; c < 4; c++)
-        f[c] = fmaf(256.f, __int_as_float(hi[c]) - MAGIC_F, __int_as_float(lo[c]) - MAGIC_F);
+      for (int c = 0; c < 4; c++) {
+        const float h = fmaf(0.0625f, __int_as_float(ho[c]) - MAGIC_F, __int_as_float(he[c]) - MAGIC_F);
+        const float l = fmaf(0.0625f, __int_as_float(lo[c]) - MAGIC_F, __int_as_float(le[c]) - MAGIC_F);
+        f[c] = fmaf(256.f, h, l);
+      }
     } else {
 #pragma unroll
       for (int c = 0; c < 4; c++) f[c] = 0.f;
@@ -565,6 +677,7 @@ struct WarpAttn {
     }
     const float i0 = t0 >= 0x1p-110f ? __fdividef(65535.f, t0) : 0.f;
     const float i1 = t1 >= 0x1p-110f ? __fdividef(65535.f, t1) : 0.f;
+    uint32_t hb[4], lb[4];
     uint32_t lo[NSUP], hi[NSUP];  // bytes of column g's weights of the tile's rows 2t, 2t + 1, 8 + 2t, 8 + 2t + 1
 #pragma unroll
     for (int sp = 0; sp < NSUP; sp++) {
@@ -575,40 +688,38 @@ struct WarpAttn {
       hi[sp] = __byte_perm(x0, x1, 0x7531);
     }
     const int start[4] = {MAGIC, MAGIC, MAGIC, MAGIC};
-    int ah[4][4], al[4][4];
+    uint32_t vt[4][4];  // byte c of a tile's four keys: channels 8g + 2c (low) and 8g + 2c + 1 (high)
 #pragma unroll
-    for (int j = 0; j < 2; j++) {  // two 16-key tiles a product
-      uint32_t T[2][4];  // byte c of the four keys: channels 8g + 2c (low) and 8g + 2c + 1 (high)
-#pragma unroll
-      for (int k = 0; k < 2; k++) {
-        uint32_t v[4];
-        v_words(blk, p, 2 * j + k, v);
-        const uint32_t a01 = __byte_perm(v[0], v[1], 0x5140), b01 = __byte_perm(v[0], v[1], 0x7362);
-        const uint32_t a23 = __byte_perm(v[2], v[3], 0x5140), b23 = __byte_perm(v[2], v[3], 0x7362);
-        T[k][0] = __byte_perm(a01, a23, 0x5410);
-        T[k][1] = __byte_perm(a01, a23, 0x7632);
-        T[k][2] = __byte_perm(b01, b23, 0x5410);
-        T[k][3] = __byte_perm(b01, b23, 0x7632);
-      }
-      const int s0 = 2 * j / NTI, s1 = (2 * j + 1) / NTI, u0 = 2 * j % NTI, u1 = (2 * j + 1) % NTI;
-      const uint32_t h0 = in_tile(hi[s0], u0), h1 = in_tile(hi[s1], u1);
-      const uint32_t l0 = in_tile(lo[s0], u0), l1 = in_tile(lo[s1], u1);
-#pragma unroll
-      for (int mt = 0; mt < 4; mt++) {
-        const uint32_t f[4] = {T[0][mt] & 0x0f0f0f0fu, (T[0][mt] >> 4) & 0x0f0f0f0fu, T[1][mt] & 0x0f0f0f0fu,
-                               (T[1][mt] >> 4) & 0x0f0f0f0fu};
-        mma16832<false>(ah[mt], f, h0, h1, j == 0 ? start : ah[mt]);
-        mma16832<false>(al[mt], f, l0, l1, j == 0 ? start : al[mt]);
-      }
+    for (int k = 0; k < 4; k++) {
+      uint32_t v[4];
+      v_words(blk, p, k, v);
+      const uint32_t a01 = __byte_perm(v[0], v[1], 0x5140), b01 = __byte_perm(v[0], v[1], 0x7362);
+      const uint32_t a23 = __byte_perm(v[2], v[3], 0x5140), b23 = __byte_perm(v[2], v[3], 0x7362);
+      vt[k][0] = __byte_perm(a01, a23, 0x5410);
+      vt[k][1] = __byte_perm(a01, a23, 0x7632);
+      vt[k][2] = __byte_perm(b01, b23, 0x5410);
+      vt[k][3] = __byte_perm(b01, b23, 0x7632);
+      hb[k] = in_tile(hi[k / NTI], k % NTI);
+      lb[k] = in_tile(lo[k / NTI], k % NTI);
     }
     const float e0 = t0 * (1.f / 65535.f), e1 = t1 * (1.f / 65535.f);
+    const float e[4] = {e0, e1, e0 * 0.0625f, e1 * 0.0625f};
 #pragma unroll
-    for (int mt = 0; mt < 4; mt++)
+    for (int mt = 0; mt < 4; mt++) {
+      int ah[4], al[4];
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {  // two 16-key tiles a product
+        const uint32_t f[4] = {vt[j][mt] & 0x0f0f0f0fu, vt[j][mt] & 0xf0f0f0f0u, vt[j + 1][mt] & 0x0f0f0f0fu,
+                               vt[j + 1][mt] & 0xf0f0f0f0u};  // odd channels: 16 c
+        mma16832<false>(ah, f, hb[j], hb[j + 1], j == 0 ? start : ah);
+        mma16832<false>(al, f, lb[j], lb[j + 1], j == 0 ? start : al);
+      }
 #pragma unroll
       for (int c = 0; c < 4; c++) {
-        const float v = fmaf(256.f, __int_as_float(ah[mt][c]) - MAGIC_F, __int_as_float(al[mt][c]) - MAGIC_F);
-        o[p][mt][c] = fmaf(c & 1 ? e1 : e0, v, o[p][mt][c]);
+        const float v = fmaf(256.f, __int_as_float(ah[c]) - MAGIC_F, __int_as_float(al[c]) - MAGIC_F);
+        o[p][mt][c] = fmaf(e[c], v, o[p][mt][c]);
       }
+    }
   }
 
   // the same with float32 weights in three bf16 terms; o holds channels 8g + mt and 8g + 4 + mt
@@ -893,12 +1004,13 @@ __device__ __forceinline__ int warp_incl_sum(int v) {
   }
   return v;
 }
-// blocks of all items; per_seq items a sequence
-__device__ __forceinline__ int total_blocks(const AttnArgs &a, int per_seq) {
-  int s = 0;
-  for (int i = threadIdx.x & 31; i < a.B; i += 32) s += (keys_of(a, i, false) + KV4_BLOCK - 1) / KV4_BLOCK;
-  return __reduce_add_sync(0xffffffffu, s) * per_seq;
+// Starting and ending an item costs a warp about as much as ITEM_COST blocks (q, the joins): an item
+// of n blocks counts as n + ITEM_COST, its blocks being the last n.
+constexpr int ITEM_COST = 2;
+__device__ __forceinline__ int blocks_of(const AttnArgs &a, int b) {
+  return (keys_of(a, b, false) + KV4_BLOCK - 1) / KV4_BLOCK;
 }
+__device__ __forceinline__ int cost_of(int blocks) { return blocks > 0 ? blocks + ITEM_COST : 0; }
 
 template <typename T, int NG, int GP, int NW, int ST, int OCC>
 __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
@@ -924,17 +1036,19 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
   __syncthreads();
   const int gw = blockIdx.x * NW + warp;
   const int per_seq = a.Hkv * a.qchunks;
-  const int total = total_blocks(a, per_seq);
+  int total = 0;
+  for (int i = lane; i < a.B; i += 32) total += cost_of(blocks_of(a, i));
+  total = __reduce_add_sync(0xffffffffu, total) * per_seq;
   const int per = (total + a.n_warps - 1) / a.n_warps;
   const int f0 = min((long)gw * per, (long)total), f1 = min((long)f0 + per, (long)total);
   const long c0 = (long)blockIdx.x * NW * per, c1 = min(c0 + (long)NW * per, (long)total);  // of the CTA
   if (c0 >= c1) return;  // the whole CTA
   bool one = false;
   if (f0 < f1) {
-  // the sequence of block f0, and the blocks before it
+  // the sequence that f0 lies in, and the cost before it
   int b = 0, before = 0;
   for (int i0 = 0, sum = 0; i0 < a.B; i0 += 32) {
-    const int n = i0 + lane < a.B ? (keys_of(a, i0 + lane, false) + KV4_BLOCK - 1) / KV4_BLOCK * per_seq : 0;
+    const int n = i0 + lane < a.B ? cost_of(blocks_of(a, i0 + lane)) * per_seq : 0;
     const int incl = sum + warp_incl_sum(n);
     const unsigned past = __ballot_sync(0xffffffffu, incl > f0);
     if (past) {
@@ -945,55 +1059,56 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
     }
     sum = __shfl_sync(0xffffffffu, incl, 31);
   }
-  // the run, walked twice: by the issue of copies and, up to ST blocks behind it, by the arithmetic
+  // the run, walked twice: by the issue of copies (ld_) and, up to ST blocks behind it, by the
+  // arithmetic; `v` is the place of the next block in the sequence of costs
   const int cap_blk = a.cap / KV4_BLOCK;
-  auto blocks_from = [&](int &sq) {  // blocks of the first sequence from sq on that has a key
+  auto next_blocks = [&](int &sq) {  // blocks of the first sequence from sq on that has a key
     for (;; sq++) {
-      const int nb = (keys_of(a, sq, false) + KV4_BLOCK - 1) / KV4_BLOCK;
+      const int nb = blocks_of(a, sq);
       if (nb > 0) return nb;
     }
   };
-  int nb = blocks_from(b);
-  int it = (f0 - before) / nb, blk = (f0 - before) % nb;
-  {
-    const int i0 = before + it * nb;  // the item of the warp's first block
-    one = i0 <= c0 && c1 <= i0 + nb && per < nb;
-  }
+  int nb = blocks_of(a, b);
+  int it = (f0 - before) / cost_of(nb);
+  const int first = before + it * cost_of(nb) + ITEM_COST;  // place of the item's block 0
+  int v = max(f0, first), blk = v - first;
+  one = first <= c0 && c1 <= first + nb && per < nb;
   Ring<BLK, ST> ring{ring_mem + warp * ST * BLK, bars + warp * ST, &s_abort, a.err};
-  const int n = f1 - f0;
-  int issued = 0, ld_b = b, ld_it = it, ld_nb = nb, ld_left = nb - blk;
+  int issued = 0, ld_v = v, ld_b = b, ld_it = it, ld_nb = nb, ld_left = nb - blk;
   const uint8_t *ld = a.data + ((long)(b * a.Hkv + it / a.qchunks) * cap_blk + blk) * BLK;
   auto issue_next = [&]() {
     if (lane == 0) ring.issue(issued, ld);
     issued++;
+    ld_v++;
     ld += BLK;
-    if (--ld_left == 0 && issued < n) {  // the next item
+    if (--ld_left == 0 && ld_v < f1) {  // the next item
+      ld_v += ITEM_COST;
       if (++ld_it == per_seq) {
         ld_it = 0;
         ld_b++;
-        ld_nb = blocks_from(ld_b);
+        ld_nb = next_blocks(ld_b);
       }
       ld_left = ld_nb;
       ld = a.data + (long)(ld_b * a.Hkv + ld_it / a.qchunks) * cap_blk * BLK;
     }
   };
-  for (int i = 0; i < ST && i < n; i++) issue_next();
+  for (int i = 0; i < ST && ld_v < f1; i++) issue_next();
   W w;
-  for (int i = 0; i < n;) {  // segments of one item each
+  for (int i = 0; v < f1;) {  // segments of one item each
     const int kvh = it / a.qchunks, qc = it % a.qchunks;
     const int head0 = kvh * a.G + qc * GP, nq = min(GP, a.G - qc * GP);
     const int nkeys = keys_of(a, b, false);
-    const int take = min(nb - blk, n - i);
+    const int take = min(nb - blk, f1 - v);
     w.start(reinterpret_cast<const T *>(a.q) + (long)b * a.ldq + (long)head0 * D, nq, a.scale_log2);
     for (int k = 0; k < take; k++, i++) {
       if (!ring.wait(i)) {
         if (lane == 0) ring.drain(i, issued);
-        i = n;
+        v = f1;
         break;
       }
       w.block(ring.mem + (i % ST) * BLK, (blk + k) * KV4_BLOCK, nkeys);
       __syncwarp();
-      if (issued < n) issue_next();  // into the stage just read
+      if (ld_v < f1) issue_next();  // into the stage just read
     }
     w.join();
     if (2 * t < GP) {
@@ -1040,11 +1155,15 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
           }
       }
     }
-    blk = 0;
-    if (i < n && ++it == per_seq) {
-      it = 0;
-      b++;
-      nb = blocks_from(b);
+    v += take;
+    if (v < f1) {  // the next item
+      v += ITEM_COST;
+      blk = 0;
+      if (++it == per_seq) {
+        it = 0;
+        b++;
+        nb = next_blocks(b);
+      }
     }
   }
   } else if (warp > 0 && lane < GP) {  // no blocks: nothing to add to the CTA's item
@@ -1092,17 +1211,17 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a, int share) {
   const int b = live ? (int)(out / Hq) : 0, head = live ? (int)(out % Hq) : 0;
   const int kvh = head / a.G, qh = head % a.G;
   const int it = kvh * a.qchunks + qh / GP;
-  int sum = 0, upto = 0;  // blocks of all sequences, and of those before b
+  int sum = 0, upto = 0;  // cost of all sequences, and of those before b
   for (int i = lane; i < a.B; i += 32) {
-    const int nb = (keys_of(a, i, false) + KV4_BLOCK - 1) / KV4_BLOCK;
-    sum += nb;
-    upto += i < b ? nb : 0;
+    const int n = cost_of(blocks_of(a, i));
+    sum += n;
+    upto += i < b ? n : 0;
   }
   sum = __reduce_add_sync(0xffffffffu, sum) * per_seq;
   upto = __reduce_add_sync(0xffffffffu, upto) * per_seq;
-  const int nb = (keys_of(a, b, false) + KV4_BLOCK - 1) / KV4_BLOCK;
+  const int nb = blocks_of(a, b);
   const int per = (sum + a.n_warps - 1) / a.n_warps;
-  const int s = upto + it * nb;  // blocks s .. s + nb - 1
+  const int s = upto + it * cost_of(nb) + ITEM_COST;  // places of the blocks: s .. s + nb - 1
   const int w0 = nb ? s / per : 0, w1 = nb ? (s + nb - 1) / per : 0;
   float m = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
@@ -1126,12 +1245,12 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a, int share) {
       const int w = j < nA ? w0 + j : j < nA + mid ? (cA + 1 + j - nA) * SNW : cB * SNW + j - nA - mid;
       return base + w * step;
     };
-    // four slots a step, their loads in flight together
-    for (int i = part_of; i < n; i += 4 * share) {
-      float2 ml[4];
-      float v[4][C];
+    // eight slots a step, their loads in flight together
+    for (int i = part_of; i < n; i += 8 * share) {
+      float2 ml[8];
+      float v[8][C];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < 8; k++) {
         const int j = i + k * share;
         ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
@@ -1150,13 +1269,13 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a, int share) {
       }
       float mn = m;
 #pragma unroll
-      for (int k = 0; k < 4; k++) mn = fmaxf(mn, ml[k].x);
+      for (int k = 0; k < 8; k++) mn = fmaxf(mn, ml[k].x);
       const float al = m == -INFINITY ? 1.f : tc::ex2(m - mn);
       l *= al;
 #pragma unroll
       for (int c = 0; c < C; c++) acc[c] *= al;
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < 8; k++) {
         const float f = ml[k].x == -INFINITY ? 1.f : tc::ex2(ml[k].x - mn);
         l = fmaf(f, ml[k].y, l);
 #pragma unroll
@@ -1230,8 +1349,13 @@ RowArgs row_args(const Kv4Cache &c, const Kv4Rows &r) {
   a.cu = r.cu; a.start = r.start; a.n_rows = r.n_rows; a.zero_rest = r.zero_rest; a.err = r.err;
   return a;
 }
-dim3 row_grid(const RowArgs &a) {
-  return dim3((a.n_rows + ROWS_T - 1) / ROWS_T, (a.Hkv * a.ng + 7) / 8, 2);
+dim3 row_grid(const RowArgs &a, int rows) {
+  return dim3((a.n_rows + rows - 1) / rows, (a.Hkv * a.ng + 7) / 8, 2);
+}
+// 64 rows a CTA from two CTAs an SM on
+bool many_rows(const RowArgs &a) {
+  const dim3 g = row_grid(a, 64);
+  return (long)g.x * g.y * g.z >= 2 * 148;
 }
 
 int device_sms() {
@@ -1260,7 +1384,7 @@ int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
   a.qchunks = (a.G + GP - 1) / GP;
   const long items = (long)a.B * a.Hkv * a.qchunks;
   const int nblk = a.cap / KV4_BLOCK;
-  if (items * nblk >= 0x7fffffffL) return DREAMER_ERR_UNSUPPORTED;
+  if (items * (nblk + ITEM_COST) >= 0x7fffffffL) return DREAMER_ERR_UNSUPPORTED;
   if (use_split(items, nblk)) {
     using C = SplitCfg<T, NG>;
     const int grid = device_sms() * C::OCC;
@@ -1299,15 +1423,19 @@ int dispatch_attn(const AttnArgs &a, cudaStream_t s, LaunchOpt o) {
 int kv4_store(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o) {
   if (r.n_rows == 0) return DREAMER_OK;
   const RowArgs a = row_args(c, r);
-  return r.dtype == 0 ? launch(kv4_store_kernel<float>, row_grid(a), dim3(256), 0, 1, s, o, a)
-                      : launch(kv4_store_kernel<bf16>, row_grid(a), dim3(256), 0, 1, s, o, a);
+  const bool many = many_rows(a);
+  auto go = [&](void (*kern)(RowArgs)) { return launch(kern, row_grid(a, many ? 64 : 16), dim3(256), 0, 1, s, o, a); };
+  if (r.dtype == 0) return go(many ? kv4_store_kernel<float, 64> : kv4_store_kernel<float, 16>);
+  return go(many ? kv4_store_kernel<bf16, 64> : kv4_store_kernel<bf16, 16>);
 }
 
 int kv4_load(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o) {
   if (r.n_rows == 0) return DREAMER_OK;
   const RowArgs a = row_args(c, r);
-  return r.dtype == 0 ? launch(kv4_load_kernel<float>, row_grid(a), dim3(256), 0, 1, s, o, a)
-                      : launch(kv4_load_kernel<bf16>, row_grid(a), dim3(256), 0, 1, s, o, a);
+  const bool many = many_rows(a);
+  auto go = [&](void (*kern)(RowArgs)) { return launch(kern, row_grid(a, many ? 64 : 16), dim3(256), 0, 1, s, o, a); };
+  if (r.dtype == 0) return go(many ? kv4_load_kernel<float, 64> : kv4_load_kernel<float, 16>);
+  return go(many ? kv4_load_kernel<bf16, 64> : kv4_load_kernel<bf16, 16>);
 }
 
 int kv4_attn(const Kv4Cache &c, const Kv4Attn &t, cudaStream_t s, LaunchOpt o) {
