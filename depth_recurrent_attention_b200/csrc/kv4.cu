@@ -49,11 +49,15 @@ struct RowArgs {
   int *err;
 };
 
-// Block (of head 0) and position in the sequence of the CTA's rows: row r belongs to the sequence b
-// with cu[b] <= r < cu[b + 1].  A position below 0: the row is in no sequence, or its place is outside
-// the cache (reported).
+// Place in the cache of the CTA's rows: byte offset of a row's codes in head 0's plane 0, and of its
+// pair from there on.  Row r belongs to the sequence b with cu[b] <= r < cu[b + 1]; an offset below 0: the
+// row is in no sequence, or its position is outside the cache (reported).
+struct Place {
+  long codes;
+  int pair;
+};
 template <int ROWS>
-__device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu, long *blk, int *pos) {
+__device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu, Place *place) {
   const int tid = threadIdx.x;
   const int *cu = a.cu;
   if (a.cu && a.B <= CU_SMEM) {
@@ -85,8 +89,9 @@ __device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu,
         else raise_dev_error(a.err, DEV_BAD_INDEX);
       }
     }
-    pos[tid] = p;
-    blk[tid] = p < 0 ? 0 : (long)b * a.Hkv * (a.cap / KV4_BLOCK) + p / KV4_BLOCK;
+    const int t = p % KV4_BLOCK;
+    place[tid].codes = p < 0 ? -1 : ((long)b * a.Hkv * (a.cap / KV4_BLOCK) + p / KV4_BLOCK) * (a.ng * 2 * (PLANE + PAIRS)) + t * 32;
+    place[tid].pair = 2 * a.ng * PLANE - t * (32 - 4);
   }
   __syncthreads();
 }
@@ -135,10 +140,14 @@ template <> struct Raw8<bf16> {
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
+  static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
   __device__ __forceinline__ void range(float &mx, float &neg) const {
-    const uint32_t sign = 0x80008000u;
     const uint32_t hi = max2(max2(u[0], u[1]), max2(u[2], u[3]));
-    const uint32_t lo = max2(max2(u[0] ^ sign, u[1] ^ sign), max2(u[2] ^ sign, u[3] ^ sign));
+    const uint32_t lo = min2(min2(u[0], u[1]), min2(u[2], u[3])) ^ 0x80008000u;
     // (max, max of the negated) in the two halves of a word
     uint32_t r = max2(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
 #pragma unroll
@@ -170,7 +179,7 @@ __device__ __noinline__ float code_exact(float x, float m, float s) {
 // (max - min) / 15 in 64 bits
 __device__ __noinline__ float step_exact(float mx, float mn) { return (float)(((double)mx - (double)mn) / 15.0); }
 
-// Eight codes of a lane's values, four bits each.  The quotient in 32 bits is off by less than 2^-19,
+// Eight codes of a lane's values, four bits each.  The quotient in 32 bits is off by less than 2^-18,
 // so it rounds as the exact one does unless that lies within 2^-16 of a half, which the remainder
 // d - c s (exact: at most 20 bits) shows.  There the remainder decides where d = x - m is
 // exact, as it nearly always is for bfloat16 (a tie goes to the even code), else the form in 64 bits.
@@ -178,32 +187,44 @@ __device__ __noinline__ float step_exact(float mx, float mn) { return (float)(((
 template <typename T>
 __device__ __forceinline__ uint32_t codes8(const Raw8<T> &x, float m, float s) {
   constexpr bool CLAMP = sizeof(T) == 4;
-  const float inv = 1.0f / s, near = s * (0.5f - 0x1p-16f);
+  float inv;  // within 2^-23
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float near = s * (0.5f - 0x1p-16f);
+  const uint64_t inv2 = f2_pack(inv, inv), s2 = f2_pack(s, s), magic2 = f2_pack(12582912.f, 12582912.f);
+  const uint64_t minus1 = f2_pack(-1.f, -1.f);
   uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    const float d = x.minus(e, m);
-    float n;  // 1.5 * 2^23 + the rounded quotient, half to even
-    bool in = true;
+  for (int e = 0; e < 8; e += 2) {
+    const uint64_t d2 = f2_pack(x.minus(e, m), x.minus(e + 1, m));
+    uint64_t n2;  // 1.5 * 2^23 + the rounded quotients, half to even
+    bool in[2] = {true, true};
     if (CLAMP) {
-      const float y = fminf(fmaxf(d * inv, 0.f), 15.f);
-      n = y + 12582912.f;
-      in = y > 0.f && y < 15.f;
+      float2 y = f2_unpack(d2);
+      y.x = fminf(fmaxf(y.x * inv, 0.f), 15.f);
+      y.y = fminf(fmaxf(y.y * inv, 0.f), 15.f);
+      in[0] = y.x > 0.f && y.x < 15.f;
+      in[1] = y.y > 0.f && y.y < 15.f;
+      n2 = f2_add(f2_pack(y.x, y.y), magic2);
     } else {
-      n = fmaf(d, inv, 12582912.f);
+      n2 = f2_fma(d2, inv2, magic2);
     }
-    const float t = fmaf(12582912.f - n, s, d);
-    if (fabsf(t) >= near && in) {
-      const float v = x.value(e), h = 0.5f * s;
-      if (d + m == v && v - d == m) {
-        const bool odd = __float_as_uint(n) & 1u;
-        if (t > h || (t == h && odd)) n += 1.f;
-        else if (t < -h || (t == -h && odd)) n -= 1.f;
-      } else {
-        n = code_exact(v, m, s) + 12582912.f;
+    const float2 t2 = f2_unpack(f2_fma(f2_fma(n2, minus1, magic2), s2, d2)), nn = f2_unpack(n2), dd = f2_unpack(d2);
+    float n[2] = {nn.x, nn.y};
+    const float t[2] = {t2.x, t2.y}, d[2] = {dd.x, dd.y};
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      if (fabsf(t[k]) >= near && in[k]) {
+        const float v = x.value(e + k), h = 0.5f * s;
+        if (d[k] + m == v && v - d[k] == m) {
+          const bool odd = __float_as_uint(n[k]) & 1u;
+          if (t[k] > h || (t[k] == h && odd)) n[k] += 1.f;
+          else if (t[k] < -h || (t[k] == -h && odd)) n[k] -= 1.f;
+        } else {
+          n[k] = code_exact(v, m, s) + 12582912.f;
+        }
       }
+      w += __float_as_uint(n[k]) << (4 * (e + k));
     }
-    w += __float_as_uint(n) << (4 * e);
   }
   // the sum of 0x4B400000 << 4 e
   constexpr uint32_t base = 0x4B400000u + 0xB4000000u + 0x40000000u;
@@ -215,10 +236,9 @@ __global__ void __launch_bounds__(256) kv4_store_kernel(RowArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ int scu[CU_SMEM + 1];
-  __shared__ long sblk[ROWS];
-  __shared__ int spos[ROWS];
+  __shared__ Place place[ROWS];
   const int row0 = blockIdx.x * ROWS;
-  find_slots<ROWS>(a, row0, scu, sblk, spos);
+  find_slots<ROWS>(a, row0, scu, place);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.y * 8 + warp;  // head * ng + plane
   if (hp >= a.Hkv * a.ng) return;
@@ -230,25 +250,26 @@ __global__ void __launch_bounds__(256) kv4_store_kernel(RowArgs a) {
                  (long)(row0 + sub) * ld;
   const int block_bytes = a.ng * 2 * (PLANE + PAIRS);
   uint8_t *dst = a.data + (long)head * (a.cap / KV4_BLOCK) * block_bytes + (side * a.ng + plane) * PLANE + (lane & 7) * 4;
-  // from a row's codes (of lane 0 of its 8) to its pair: + pair_at + t * (4 - 32)
-  const int pair_at = 2 * a.ng * PLANE + (side * a.ng + plane) * (PAIRS - PLANE);
+  const int pair_at = (side * a.ng + plane) * (PAIRS - PLANE);
   Raw8<T> next;
   next.zero();
-  if (spos[sub] >= 0) next.load(src);
+  if (place[sub].codes >= 0) next.load(src);
 #pragma unroll 1
   for (int r = 0; r < ROWS; r += 4) {
     const Raw8<T> x = next;
-    const int p = spos[r + sub];
+    const Place pl = place[r + sub];
     src += 4 * ld;
-    if (r + 4 < ROWS && spos[r + 4 + sub] >= 0) next.load(src);  // the next rows', in flight meanwhile
+    if (r + 4 < ROWS && place[r + 4 + sub].codes >= 0) next.load(src);  // the next rows', in flight meanwhile
     float mx, neg;
     x.range(mx, neg);
     // s = bf16((max - min) / 15): in 32 bits off by 2 steps at most, so a rounding within 4 of a tie is
     // taken in 64
     float sf = (mx + neg) * (1.0f / 15.0f);
     if ((((__float_as_uint(sf) + 4u) & 0xffffu) - 0x8000u) <= 8u || sf < 0x1p-100f) sf = step_exact(mx, -neg);
-    float s = __bfloat162float(__float2bfloat16_rn(sf)), m = __bfloat162float(__float2bfloat16_rn(-neg));
-    if (!(fmaxf(mx, neg) <= 0x1p126f) || !(mx + neg >= 0.f)) s = m = NAN;  // NaN, infinite, out of range
+    uint32_t pr = bf2_pack_rn(sf, -neg);
+    // NaN, infinite, out of range
+    if (!(fmaxf(mx, neg) <= 0x1p126f) || !(mx + neg >= 0.f)) pr = 0x7fff7fffu;
+    const float s = __uint_as_float(pr << 16), m = __uint_as_float(pr & 0xffff0000u);
     uint32_t w = 0;
     if (s >= 0x1p-100f) {
       w = codes8<T>(x, m, s);
@@ -256,12 +277,10 @@ __global__ void __launch_bounds__(256) kv4_store_kernel(RowArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; e++) w |= (uint32_t)code_exact(x.value(e), m, s) << (4 * e);
     }
-    if (p >= 0) {
-      const int t = p % KV4_BLOCK;
-      uint8_t *q = dst + sblk[r + sub] * block_bytes + t * 32;
+    if (pl.codes >= 0) {
+      uint8_t *q = dst + pl.codes;
       *reinterpret_cast<uint32_t *>(q) = w;
-      if ((lane & 7) == 0)
-        *reinterpret_cast<uint32_t *>(q + pair_at - t * 28) = bf2_pack_rn(s, m);
+      if ((lane & 7) == 0) *reinterpret_cast<uint32_t *>(q + pair_at + pl.pair) = pr;
     }
   }
 }
@@ -271,10 +290,9 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ int scu[CU_SMEM + 1];
-  __shared__ long sblk[ROWS];
-  __shared__ int spos[ROWS];
+  __shared__ Place place[ROWS];
   const int row0 = blockIdx.x * ROWS;
-  find_slots<ROWS>(a, row0, scu, sblk, spos);
+  find_slots<ROWS>(a, row0, scu, place);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.y * 8 + warp;
   if (hp >= a.Hkv * a.ng) return;
@@ -283,26 +301,26 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
   T *dst = reinterpret_cast<T *>(const_cast<void *>(side ? a.v : a.k)) + (long)hp * KV4_GROUP + (lane & 7) * 8;
   const long ld = side ? a.ldv : a.ldk;
   const int sub = lane >> 3;
-  const long head_blk = (long)head * (a.cap / KV4_BLOCK);
-  const int block_bytes = a.ng * 2 * (PLANE + PAIRS);
+  const int block_bytes = a.ng * 2 * (PLANE + PAIRS), sp = side * a.ng + plane;
+  const uint8_t *from = a.data + (long)head * (a.cap / KV4_BLOCK) * block_bytes + sp * PLANE;
 #pragma unroll 1
   for (int r0 = 0; r0 < ROWS; r0 += 16) {
     uint32_t w[4], pr[4];
-    int p[4];
+    bool in[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      p[i] = spos[r0 + i * 4 + sub];
+      const Place pl = place[r0 + i * 4 + sub];
+      in[i] = pl.codes >= 0;
       w[i] = pr[i] = 0;
-      if (p[i] < 0) continue;
-      const uint8_t *blk = a.data + (sblk[r0 + i * 4 + sub] + head_blk) * block_bytes;
-      const int t = p[i] % KV4_BLOCK;
-      w[i] = *reinterpret_cast<const uint32_t *>(blk + (side * a.ng + plane) * PLANE + t * 32 + (lane & 7) * 4);
-      pr[i] = *reinterpret_cast<const uint32_t *>(blk + 2 * a.ng * PLANE + (side * a.ng + plane) * PAIRS + t * 4);
+      if (!in[i]) continue;
+      const uint8_t *q = from + pl.codes;
+      w[i] = *reinterpret_cast<const uint32_t *>(q + (lane & 7) * 4);
+      pr[i] = *reinterpret_cast<const uint32_t *>(q + pl.pair + sp * (PAIRS - PLANE));
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int r = row0 + r0 + i * 4 + sub;
-      if (p[i] < 0 && !(a.zero_rest && r < a.n_rows)) continue;
+      if (!in[i] && !(a.zero_rest && r < a.n_rows)) continue;
       const float s = __uint_as_float(pr[i] << 16), m = __uint_as_float(pr[i] & 0xffff0000u);
       float x[8];
 #pragma unroll
