@@ -103,12 +103,24 @@ __device__ __forceinline__ void check_cu(const PackedArgs &a) {
 }
 
 // ---- bfloat16: tcgen05 ---------------------------------------------------------------------
-// The structure of the handle's sequence attention (tc_attn.cuh): a CTA takes one head and two
-// adjacent 128-query tiles A, B of a prompt that share every K/V block; warp 0 loads Q and K by
-// TMA, warp 2 V, warp 1 issues the MMAs, warps 3-10 hold one query row a thread.  Scores, weights
-// and outputs stay in tensor memory; the output is rescaled only when a row's maximum grows by
-// more than 2^8.  Weights enter the output product as bf16 (half a step of 2^-8 relative each, as
+// A CTA takes one head and two adjacent 128-query tiles A, B of a prompt that share every K/V block;
+// warp 0 loads Q and K by TMA, warp 2 V, warp 1 issues the MMAs, warps 3-10 hold one query row a thread.
+// Scores, weights and outputs stay in tensor memory; the output is rescaled only when a row's maximum
+// grows by more than 2^8.  Weights enter the output product as bf16 (half a step of 2^-8 relative each, as
 // the stored output is), their sum is of the float32 values.
+//
+// What bounds it, in cycles of a block of 128 x 128 and one tile, by clocks read in the kernel: at head
+// dim 128 the products take 1020 and the row's part (scores out, maximum, exponentials, weights in) 1750,
+// one after the other for a tile, which two tiles overlap in part; at head dim 64 the products take
+// 960 and the row's parts of both tiles together 2900, of which the exponentials' unit is busy 2048.
+// So
+//   - head dim 64 keeps the weights in tensor-memory columns of their own, and the next block's
+//     scores are computed as soon as this block's are in registers (one sequence of 8192 tokens, 16
+//     heads of 64: 248 -> 231 us); at 128 tensor memory is full, the weights lie over their scores;
+//   - the products are issued by a converged warp's elected lane (3 to 6 % against one lane of a split
+//     warp).
+// A polynomial for a part of the exponentials (2 to 5 of every 8 pairs) cost 1 to 14 %, the weights handed
+// over in halves 4 %: neither is taken.
 template <int D>
 struct PkCfg {
   static constexpr int CH = D / 64;                 // 64-column chunks of a head
@@ -118,14 +130,37 @@ struct PkCfg {
   static constexpr int Q_BYTES = 2 * CH * TILE;     // both query tiles
   static constexpr int KV_BYTES = CH * TILE;        // one K (or V) block
   static constexpr int SMEM = Q_BYTES + (KST + VST) * KV_BYTES + 1024 + 256;
+  static constexpr bool SEP = D == 64;              // weights in columns of their own
+  static constexpr int P0 = SEP ? 256 : 0, P_STEP = SEP ? 64 : 128;   // weights of tile t: P0 + t * P_STEP
+  static constexpr int O0 = SEP ? 384 : 256;                          // output of tile t: O0 + t * D
   static_assert(SMEM <= 227 * 1024, "smem");
 };
-
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
                : "=r"(r) : "r"(taddr) : "memory");
   return r;
+}
+
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// D[tmem] (+)= A B^T with the descriptors' low words (address and leading offset) and common high word:
+// A in shared memory, or in tensor memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
 }
 
 template <int D>
@@ -135,6 +170,7 @@ __global__ void __launch_bounds__(352, 1)
   using namespace tc;
   using C = PkCfg<D>;
   constexpr int CH = C::CH, KST = C::KST, VST = C::VST;
+  constexpr bool SEP = C::SEP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = smem;
@@ -144,25 +180,20 @@ __global__ void __launch_bounds__(352, 1)
   uint64_t *q_full = bars;
   uint64_t *k_full = q_full + 1, *k_empty = k_full + KST;
   uint64_t *v_full = k_empty + KST, *v_empty = v_full + VST;
-  uint64_t *s_full = v_empty + VST, *p_full = s_full + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(p_full + 2);
+  // per tile: scores ready; SEP: scores in registers; weights ready; SEP: output product done
+  uint64_t *s_full = v_empty + VST, *s_read = s_full + 2, *p_full = s_read + 2, *pv_done = p_full + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pv_done + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *item_slot = reinterpret_cast<int *>(tmem_slot + 2);          // row0, length, tile
   volatile int *by_rows = reinterpret_cast<volatile int *>(tmem_slot + 5);  // [2] diagonal block on CUDA cores
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % a.Hq;
-  pdl_wait();  // inputs of the previous kernel are visible from here on
-  if (warp == 0) {
-    if (blockIdx.x == 0) check_cu(a);
-    const int3 it = find_item<256>(a, blockIdx.x / a.Hq);
-    if (lane == 0) {
-      item_slot[0] = it.x;
-      item_slot[1] = it.y;
-      item_slot[2] = it.z;
-    }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
   }
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 64) {
     mbar_init(smem_u32(q_full), 1);
     for (int s = 0; s < KST; s++) {
       mbar_init(smem_u32(&k_full[s]), 1);
@@ -174,7 +205,9 @@ __global__ void __launch_bounds__(352, 1)
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 128);
+      mbar_init(smem_u32(&s_read[i]), 4);
+      mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&pv_done[i]), 1);
       by_rows[i] = 0;
     }
     *abort_flag = 0;
@@ -183,27 +216,32 @@ __global__ void __launch_bounds__(352, 1)
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
-  __syncthreads();
-  const int row0 = item_slot[0], S = item_slot[1], pair = item_slot[2];
-  if (pair < 0) {  // fewer items than launched
-    pdl_trigger();
-    return;
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+  pdl_wait();  // inputs of the previous kernel are visible from here on
+  if (warp == 0) {
+    if (blockIdx.x == 0) check_cu(a);
+    const int3 it = find_item<256>(a, blockIdx.x / a.Hq);
+    if (lane == 0) {
+      item_slot[0] = it.x;
+      item_slot[1] = it.y;
+      item_slot[2] = it.z;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   pdl_trigger();  // after the TMEM allocation (see pdl_trigger)
+  const uint32_t tmem = *tmem_slot;
+  const int row0 = item_slot[0], S = item_slot[1], pair = item_slot[2];
+  if (pair < 0) {  // fewer items than launched
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
   const int qtA = 2 * pair, qtB = 2 * pair + 1;
   const bool hasB = qtB * 128 < S;
   const int nbA = qtA + 1, nbB = hasB ? qtB + 1 : 0;
   const int nb = hasB ? nbB : nbA;
-  // TMEM columns: S_A 0..127, S_B 128..255, O_A 256.., O_B 256 + D..
-  const uint32_t tS = tmem, tO = tmem + 256;
+  // TMEM columns: S_A 0..127, S_B 128..255, then see PkCfg
+  const uint32_t tS = tmem, tP = tmem + C::P0, tO = tmem + C::O0;
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------- producers (warp 0: Q, K; warp 2: V)
@@ -248,64 +286,86 @@ __global__ void __launch_bounds__(352, 1)
           }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------- MMA issuer (order as in tc_attn.cuh)
-    if (lane == 0) {
-      constexpr uint32_t ID_S = idesc_bf16_m128(128);
-      constexpr uint32_t ID_PV = idesc_bf16_m128_bmn(D);
-      bool ok = mbar_wait(smem_u32(q_full), 0, abort_flag, a.err);
-      const uint32_t q0 = smem_u32(sQ);
-      auto issue_s = [&](int t, uint32_t k0) {
-        const uint32_t qt0 = q0 + t * CH * C::TILE;
+    // ------------------------------------------------- MMA issuer
+    // Per tile S(0); then for each block j (SEP) S(j+1) once S(j) is in registers and P(j) V_j once the
+    // weights are ready, or P(j) V_j and then S(j+1) over them.  The whole warp walks the loop with
+    // values that are the same in every lane and one elected lane issues: a chain of descriptors
+    // computed by one thread of a split warp took longer than the products.
+    constexpr uint32_t ID_S = idesc_bf16_m128(128);
+    constexpr uint32_t ID_PV = idesc_bf16_m128_bmn(D);
+    constexpr uint32_t DESC_HI = (1024 >> 4) | 1u << 14 | 2u << 29;  // 8-row groups 1024 bytes apart, SW128
+    const int uA = __shfl_sync(0xffffffffu, nbA, 0), uB = __shfl_sync(0xffffffffu, nbB, 0);
+    const int un = max(uA, uB);
+    const uint32_t ut = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t q_lo = smem_u32(sQ) >> 4 | 1u << 16, k_lo = smem_u32(sK) >> 4 | 1u << 16;
+    const uint32_t v_lo = smem_u32(sV) >> 4 | (uint32_t)(C::TILE >> 4) << 16;
+    const bool one = elect_one();
+    auto wait = [&](uint64_t *bar, int n) {
+      const bool r = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), n & 1, abort_flag, a.err));
+      tc_fence_after();
+      return r;
+    };
+    auto commit = [&](uint64_t *bar) {
+      if (one) mma_commit(smem_u32(bar));
+    };
+    auto issue_s = [&](int t, int ks) {
+      if (one) {
 #pragma unroll
         for (int k = 0; k < D / 16; k++) {
-          const uint32_t off = (k >> 2) * C::TILE + (k & 3) * 32;
-          mma_bf16(tS + t * 128, desc_k128(qt0 + off), desc_k128(k0 + off), ID_S, k != 0);
+          const uint32_t off = ((k >> 2) * C::TILE + (k & 3) * 32) >> 4;
+          mma_ss(ut + t * 128, q_lo + ((t * CH * C::TILE) >> 4) + off, k_lo + ks * (C::KV_BYTES >> 4) + off, DESC_HI, ID_S, k != 0);
         }
-      };
-      if (ok && mbar_wait(smem_u32(&k_full[0]), 0, abort_flag, a.err)) {
-        tc_fence_after();
-        const uint32_t k0 = smem_u32(sK);
-        issue_s(0, k0);
-        mma_commit(smem_u32(&s_full[0]));
-        if (nbB > 0) {
-          issue_s(1, k0);
-          mma_commit(smem_u32(&s_full[1]));
-        }
-        mma_commit(smem_u32(&k_empty[0]));
-      } else {
-        ok = false;
       }
-      for (int j = 0; j < nb && ok; j++) {
-        const int vs = j % VST;
-        if (!mbar_wait(smem_u32(&v_full[vs]), (j / VST) & 1, abort_flag, a.err)) break;
-        tc_fence_after();
-        const uint32_t v0 = smem_u32(sV + vs * C::KV_BYTES);
-        const bool next = j + 1 < nb;
-        const int ks = (j + 1) % KST;
-        uint32_t k1 = 0;
-        if (next) {
-          if (!mbar_wait(smem_u32(&k_full[ks]), ((j + 1) / KST) & 1, abort_flag, a.err)) break;
-          tc_fence_after();
-          k1 = smem_u32(sK + ks * C::KV_BYTES);
-        }
-        for (int t = 0; t < 2; t++) {
-          const int nbt = t == 0 ? nbA : nbB;
-          if (j >= nbt) continue;
-          if (!mbar_wait(smem_u32(&p_full[t]), j & 1, abort_flag, a.err)) { ok = false; break; }
-          tc_fence_after();
-          if (!(j + 1 == nbt && by_rows[t])) {
+    };
+    auto issue_pv = [&](int t, int j, int vs) {  // 128 keys, 16 per instruction (8 TMEM columns of P)
+      if (j + 1 == (t == 0 ? uA : uB) && by_rows[t]) return;
+      if (one) {
 #pragma unroll
-            for (int k = 0; k < 8; k++)  // 128 keys, 16 per instruction (8 TMEM columns of P)
-              mma_bf16_ts(tO + t * D, tS + t * 128 + k * 8, desc_mn128(v0 + k * 2048, C::TILE), ID_PV,
-                          (j | k) != 0);
-          }
-          if (j + 1 < nbt) issue_s(t, k1);
-          mma_commit(smem_u32(&s_full[t]));
-        }
-        if (!ok) break;
-        mma_commit(smem_u32(&v_empty[vs]));
-        if (next) mma_commit(smem_u32(&k_empty[ks]));
+        for (int k = 0; k < 8; k++)
+          mma_ts(ut + C::O0 + t * D, ut + C::P0 + t * C::P_STEP + k * 8, v_lo + vs * (C::KV_BYTES >> 4) + k * 128, DESC_HI,
+                 ID_PV, k == 0 ? (uint32_t)j : 1u);
       }
+    };
+    bool ok = wait(q_full, 0) && wait(&k_full[0], 0);
+    if (ok) {
+      issue_s(0, 0);
+      commit(&s_full[0]);
+      if (uB > 0) {
+        issue_s(1, 0);
+        commit(&s_full[1]);
+      }
+      commit(&k_empty[0]);
+    }
+    int vs = 0, ks = 1 % KST;  // stages of block j's values and of block j + 1's keys
+    for (int j = 0; j < un && ok; j++) {
+      const bool next = j + 1 < un;
+      if (SEP && next) {
+        if (!wait(&k_full[ks], (j + 1) / KST)) break;
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+          if (ok && j + 1 < (t == 0 ? uA : uB)) {
+            ok = wait(&s_read[t], j);
+            if (ok) issue_s(t, ks);
+            if (ok) commit(&s_full[t]);
+          }
+        if (ok) commit(&k_empty[ks]);
+      }
+      if (!ok || !wait(&v_full[vs], j / VST)) break;
+      if (!SEP && next && !wait(&k_full[ks], (j + 1) / KST)) break;
+#pragma unroll
+      for (int t = 0; t < 2; t++)
+        if (ok && j < (t == 0 ? uA : uB)) {
+          ok = wait(&p_full[t], j);
+          if (!ok) break;
+          issue_pv(t, j, vs);
+          if (!SEP && j + 1 < (t == 0 ? uA : uB)) issue_s(t, ks);
+          commit(SEP ? &pv_done[t] : &s_full[t]);
+        }
+      if (!ok) break;
+      commit(&v_empty[vs]);
+      if (!SEP && next) commit(&k_empty[ks]);
+      if (++vs == VST) vs = 0;
+      if (++ks == KST) ks = 0;
     }
   } else if (warp >= 3) {
     // ------------------------------------------------- softmax (tile A: warps 3-6, B: 7-10)
@@ -318,7 +378,12 @@ __global__ void __launch_bounds__(352, 1)
       const int qi = qt * 128 + row;               // query position in the prompt
       const uint32_t lane_off = (uint32_t)(q * 32) << 16;
       const uint32_t sbuf = tS + t * 128 + lane_off;
+      const uint32_t pbuf = tP + t * C::P_STEP + lane_off;
       const uint32_t obuf = tO + t * D + lane_off;
+      // the same answer in every lane: what follows is done by whole warps
+      auto wait_warp = [&](uint64_t *bar, int n) {
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), n & 1, abort_flag, a.err));
+      };
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nbt; j++) {
@@ -326,7 +391,7 @@ __global__ void __launch_bounds__(352, 1)
         if (diag) {
           // the diagonal block's values: rows behind the prompt's end are cleared, and a value
           // that is not finite sends the block's output product to the row form below
-          ok = mbar_wait(smem_u32(&v_full[j % VST]), (j / VST) & 1, abort_flag, a.err);
+          ok = wait_warp(&v_full[j % VST], j / VST);
           bool bad = false;
           if (ok) {
             uint8_t *vr = sV + (j % VST) * C::KV_BYTES + row * 128;
@@ -348,10 +413,10 @@ __global__ void __launch_bounds__(352, 1)
               bad = (u & 0x7fff7fffu) != 0;
             }
           }
-          if (bad) by_rows[t] = 1;  // seen by the MMA warp through p_full, by this warp through s_full
+          if (bad) by_rows[t] = 1;  // seen by the MMA warp through p_full, by this warp at the end
           if (!ok) break;
         }
-        if (!mbar_wait(smem_u32(&s_full[t]), j & 1, abort_flag, a.err)) { ok = false; break; }
+        if (!wait_warp(&s_full[t], j)) { ok = false; break; }
         tc_fence_after();
         const int lim = qi - j * 128;  // diagonal block: last visible key of the row
         // the row's 128 scores into registers with four loads in flight
@@ -361,6 +426,11 @@ __global__ void __launch_bounds__(352, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < 128; c += 32) tmem_ld_fence(sv + c);
+        if (SEP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_read[t]));
+        }
         if (diag) {
 #pragma unroll
           for (int i = 0; i < 128; i++)
@@ -383,8 +453,8 @@ __global__ void __launch_bounds__(352, 1)
           alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
         }
         const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        // P = 2^(s * scale - m) as bf16 pairs (the lower key in the low half) into the first
-        // 64 columns of this tile's S in TMEM, where the P.V MMA reads it, and summed
+        // P = 2^(s * scale - m) as bf16 pairs (the lower key in the low half), where the P.V MMA
+        // reads it, and summed
         const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-m_use, -m_use);
         uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};  // four independent sums of pairs
 #pragma unroll
@@ -398,30 +468,37 @@ __global__ void __launch_bounds__(352, 1)
             rs2[e & 3] = f2_add(rs2[e & 3], f2_pack(p0, p1));
             w[e] = bf2_pack_rn(p0, p1);
           }
-          tmem_st32_nowait(sbuf + hh * 32, w);
+          if (hh == 0) {
+            // P V of block j - 1 is done with the weights, and O holds it (else: s_full said so)
+            if (SEP && j > 0) {
+              ok = wait_warp(&pv_done[t], j - 1);
+              tc_fence_after();
+            }
+            // O rescaled before P(j) V accumulates into it
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float ov[32];
+                tmem_ld32(obuf + c, ov);
+#pragma unroll
+                for (int i = 0; i < 32; i++) ov[i] *= alpha;
+                tmem_st32(obuf + c, ov);
+              }
+            }
+          }
+          tmem_st32_nowait(pbuf + hh * 32, w);
         }
         const float2 rsf = f2_unpack(f2_add(f2_add(rs2[0], rs2[1]), f2_add(rs2[2], rs2[3])));
-        const float rs = rsf.x + rsf.y;
-        // O rescaled before P_t(j) V accumulates into it (s_full of block j also means that
-        // P_t(j-1) V has completed; P_t(j) V is issued after p_full below)
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float ov[32];
-            tmem_ld32(obuf + c, ov);
-#pragma unroll
-            for (int i = 0; i < 32; i++) ov[i] *= alpha;
-            tmem_st32(obuf + c, ov);
-          }
-        }
-        l = l * alpha + rs;
+        l = l * alpha + rsf.x + rsf.y;
         m_ref = m_new;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&p_full[t]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
+        if (!ok) break;
       }
       // the commit after the last P.V: O_t is final
-      if (ok && mbar_wait(smem_u32(&s_full[t]), nbt & 1, abort_flag, a.err)) {
+      if (ok && wait_warp(SEP ? &pv_done[t] : &s_full[t], SEP ? nbt - 1 : nbt)) {
         tc_fence_after();
         const float inv = 1.0f / l;
         const bool slow = by_rows[t] != 0;
@@ -445,7 +522,7 @@ __global__ void __launch_bounds__(352, 1)
 #pragma unroll 1
             for (int kp = 0; kp < 64; kp++) {
               __syncwarp();
-              const uint32_t pw = tmem_ld1(sbuf + kp);
+              const uint32_t pw = tmem_ld1(pbuf + kp);
 #pragma unroll
               for (int hf = 0; hf < 2; hf++) {
                 const int key = 2 * kp + hf;
@@ -483,36 +560,40 @@ __global__ void __launch_bounds__(352, 1)
 }
 
 // ---- float32: CUDA cores -------------------------------------------------------------------
-// A CTA of 128 threads takes one head and 32 query rows of a prompt, keys in blocks of 64.  The
-// threads form an 8 x 16 grid: 4 rows x 4 keys of the scores and 4 rows x D / 16 columns of the
-// output each, operands in shared memory with the reduction index outermost (Q, K and the weights
-// transposed), so a step reads two or three 16-byte words for 16 or more multiply-adds.
+// A CTA takes one head and 32 query rows of a prompt; its two groups of 128 threads take the
+// 64-key blocks in turns, each with its own softmax and buffers (one group's loads run beside the
+// other's arithmetic, and a long row's chain of blocks is half as long), and join at the end.  A
+// group's threads form an 8 x 16 grid: 4 rows x 4 keys (tx, tx + 16, ..) of the scores and 4 rows x
+// D / 16 columns of the output each.  Q and K rows are padded by 4 words, so that eight rows' 16-byte
+// reads meet every bank once; a step of 4 channels reads eight words of 16 bytes for 64 multiply-adds.
 template <int D>
 struct F32Cfg {
   static constexpr int BM = 32, BN = 64;
-  static constexpr int QP = BM + 4, KP = BN + 4, PP = BM + 4;  // padded row lengths
-  static constexpr int SMEM = (D * QP + D * KP + BN * D + BN * PP) * 4;
+  static constexpr int RP = D + 4;   // padded row of Q and K
+  static constexpr int PP = BM + 4;  // padded row of the weights [key][row]
+  static constexpr int GROUP = BN * RP + BN * D + BN * PP;  // floats of a group's K, V, weights
+  static constexpr int SMEM = (BM * RP + 2 * GROUP) * 4;
 };
 
 template <int D>
-__global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
+__global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(PackedArgs a) {
   using C = F32Cfg<D>;
-  constexpr int BM = C::BM, BN = C::BN, QP = C::QP, KP = C::KP, PP = C::PP;
+  constexpr int BM = C::BM, BN = C::BN, RP = C::RP, PP = C::PP;
   constexpr int OC = D / 16;  // output columns of a thread
   extern __shared__ __align__(16) float fsm[];
-  float *sQ = fsm;            // [D][QP]
-  float *sK = sQ + D * QP;    // [D][KP]
-  float *sV = sK + D * KP;    // [BN][D]
-  float *sP = sV + BN * D;    // [BN][PP]
   __shared__ int item[3];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
+  const int group = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  float *sQ = fsm;                                // [BM][RP]
+  float *sK = fsm + BM * RP + group * C::GROUP;   // [BN][RP]
+  float *sV = sK + BN * RP;                       // [BN][D]
+  float *sP = sV + BN * D;                        // [BN][PP]
   const int head = blockIdx.x % a.Hq, kvh = head / a.G;
-  if (tid < 32) {
+  if (threadIdx.x < 32) {
     if (blockIdx.x == 0) check_cu(a);
     const int3 it = find_item<BM>(a, blockIdx.x / a.Hq);
-    if (tid == 0) {
+    if (threadIdx.x == 0) {
       item[0] = it.x;
       item[1] = it.y;
       item[2] = it.z;
@@ -522,17 +603,21 @@ __global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
   const int row0 = item[0], S = item[1], tile = item[2];
   if (tile < 0) return;
   const int q0 = tile * BM;
-  const int ty = tid >> 4, tx = tid & 15;  // rows 4 ty .., keys 4 tx .., columns tx * 4 + 64 i ..
-  const float *Q = reinterpret_cast<const float *>(a.q) + (long)(row0 + q0) * a.ldq + (long)head * D;
-  for (int e = tid; e < BM * (D / 4); e += 128) {
-    const int r = e / (D / 4), c = e % (D / 4);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (q0 + r < S) v = *reinterpret_cast<const float4 *>(Q + (long)r * a.ldq + 4 * c);
-    sQ[(4 * c) * QP + r] = v.x;
-    sQ[(4 * c + 1) * QP + r] = v.y;
-    sQ[(4 * c + 2) * QP + r] = v.z;
-    sQ[(4 * c + 3) * QP + r] = v.w;
-  }
+  const int ty = tid >> 4, tx = tid & 15;
+  // rows n of a [rows][D] matrix into padded rows; rows that do not exist become zeros
+  auto fetch = [&](const void *src, long ld, int first, int rows, int col, float *dst, int pitch, int t, int step) {
+    const float *g = reinterpret_cast<const float *>(src) + (long)row0 * ld + col;
+    for (int e = t; e < rows * (D / 4); e += step) {
+      const int r = e / (D / 4), c = e % (D / 4);
+      const bool in = first + r < S;
+      tc::cp_async16(tc::smem_u32(dst + r * pitch + 4 * c), g + (long)(in ? first + r : 0) * ld + 4 * c, in ? 16u : 0u);
+    }
+  };
+  auto landed = [] { asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory"); };
+  auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
+  fetch(a.q, a.ldq, q0, BM, head * D, sQ, RP, threadIdx.x, 256);
+  landed();
+  __syncthreads();
   float o[4][OC], m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -542,38 +627,33 @@ __global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
     for (int c = 0; c < OC; c++) o[i][c] = 0.f;
   }
   const int last = min(S, q0 + BM);  // keys of the tile's last row
-  for (int k0 = 0; k0 < last; k0 += BN) {
-    __syncthreads();
-    const float *K = reinterpret_cast<const float *>(a.k) + (long)(row0 + k0) * a.ldk + (long)kvh * D;
-    const float *V = reinterpret_cast<const float *>(a.v) + (long)(row0 + k0) * a.ldv + (long)kvh * D;
-    for (int e = tid; e < BN * (D / 4); e += 128) {
-      const int r = e / (D / 4), c = e % (D / 4);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
-      if (k0 + r < S) {
-        v = *reinterpret_cast<const float4 *>(K + (long)r * a.ldk + 4 * c);
-        w = *reinterpret_cast<const float4 *>(V + (long)r * a.ldv + 4 * c);
-      }
-      sK[(4 * c) * KP + r] = v.x;
-      sK[(4 * c + 1) * KP + r] = v.y;
-      sK[(4 * c + 2) * KP + r] = v.z;
-      sK[(4 * c + 3) * KP + r] = v.w;
-      *reinterpret_cast<float4 *>(sV + r * D + 4 * c) = w;
-    }
-    __syncthreads();
+  for (int k0 = group * BN; k0 < last; k0 += 2 * BN) {
+    group_sync();  // the block before is done with
+    fetch(a.k, a.ldk, k0, BN, kvh * D, sK, RP, tid, 128);
+    fetch(a.v, a.ldv, k0, BN, kvh * D, sV, D, tid, 128);
+    landed();
+    group_sync();
     float s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int j = 0; j < 4; j++) s[i][j] = 0.f;
-#pragma unroll 8
-    for (int d = 0; d < D; d++) {
-      const float4 qv = *reinterpret_cast<const float4 *>(sQ + d * QP + 4 * ty);
-      const float4 kv = *reinterpret_cast<const float4 *>(sK + d * KP + 4 * tx);
-      const float qa[4] = {qv.x, qv.y, qv.z, qv.w}, ka[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      float4 qa[4], ka[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) qa[i] = *reinterpret_cast<const float4 *>(sQ + (4 * ty + i) * RP + d);
+#pragma unroll
+      for (int j = 0; j < 4; j++) ka[j] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * RP + d);
 #pragma unroll
       for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) s[i][j] = fmaf(qa[i], ka[j], s[i][j]);
+        for (int j = 0; j < 4; j++) {
+          s[i][j] = fmaf(qa[i].x, ka[j].x, s[i][j]);
+          s[i][j] = fmaf(qa[i].y, ka[j].y, s[i][j]);
+          s[i][j] = fmaf(qa[i].z, ka[j].z, s[i][j]);
+          s[i][j] = fmaf(qa[i].w, ka[j].w, s[i][j]);
+        }
     }
     const bool diag = k0 + BN > q0;  // some key of the block is behind some row
 #pragma unroll
@@ -582,7 +662,7 @@ __global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         s[i][j] *= a.scale_log2;
-        if (diag && k0 + 4 * tx + j > q0 + 4 * ty + i) s[i][j] = -INFINITY;
+        if (diag && k0 + tx + 16 * j > q0 + 4 * ty + i) s[i][j] = -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
 #pragma unroll
@@ -595,7 +675,6 @@ __global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
       for (int j = 0; j < 4; j++) {
         s[i][j] = exp2f(s[i][j] - base);
         ps += s[i][j];
-        sP[(4 * tx + j) * PP + 4 * ty + i] = s[i][j];
       }
       if (mn != m[i]) {
         l[i] *= alpha;
@@ -605,6 +684,9 @@ __global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
       l[i] += ps;
       m[i] = mn;
     }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      *reinterpret_cast<float4 *>(sP + (tx + 16 * j) * PP + 4 * ty) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
     __syncwarp();  // a row's weights are written and read by the same half warp
     const int nk = min(BN, last - k0);
     auto out_step = [&](int k, auto dtag) {
@@ -637,8 +719,29 @@ __global__ void __launch_bounds__(128) packed_f32_kernel(PackedArgs a) {
       for (int k = 0; k < nk; k++) out_step(k, std::true_type());
     }
   }
+  // the second group's sums over its own buffers, where the first one takes them in
+  float *x = fsm + BM * RP + C::GROUP;  // [4 * OC + 8][128]
+  static_assert(C::GROUP >= (4 * OC + 8) * 128, "join buffer");
+  if (group == 1) {
+    group_sync();
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+#pragma unroll
+      for (int c = 0; c < OC; c++) x[(i * OC + c) * 128 + tid] = o[i][c];
+      x[(4 * OC + i) * 128 + tid] = m[i];
+      x[(4 * OC + 4 + i) * 128 + tid] = l[i];
+    }
+  }
+  __syncthreads();
+  if (group == 1) return;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
+    const float m1 = x[(4 * OC + i) * 128 + tid], mn = fmaxf(m[i], m1);
+    // a group without a key holds zeros
+    const float f0 = m[i] == -INFINITY ? 1.f : exp2f(m[i] - mn), f1 = m1 == -INFINITY ? 1.f : exp2f(m1 - mn);
+    l[i] = fmaf(f1, x[(4 * OC + 4 + i) * 128 + tid], l[i] * f0);
+#pragma unroll
+    for (int c = 0; c < OC; c++) o[i][c] = fmaf(f1, x[(i * OC + c) * 128 + tid], o[i][c] * f0);
 #pragma unroll
     for (int k = 1; k < 16; k <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
     const int r = q0 + 4 * ty + i;
@@ -734,10 +837,10 @@ int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
   }
   const long items = most_tiles(p.n_tokens, p.n_seq, 32) * p.Hq;
   switch (p.d) {
-    case 16: return launch_packed(packed_f32_kernel<16>, items, 128, F32Cfg<16>::SMEM, s, o, a);
-    case 32: return launch_packed(packed_f32_kernel<32>, items, 128, F32Cfg<32>::SMEM, s, o, a);
-    case 64: return launch_packed(packed_f32_kernel<64>, items, 128, F32Cfg<64>::SMEM, s, o, a);
-    default: return launch_packed(packed_f32_kernel<128>, items, 128, F32Cfg<128>::SMEM, s, o, a);
+    case 16: return launch_packed(packed_f32_kernel<16>, items, 256, F32Cfg<16>::SMEM, s, o, a);
+    case 32: return launch_packed(packed_f32_kernel<32>, items, 256, F32Cfg<32>::SMEM, s, o, a);
+    case 64: return launch_packed(packed_f32_kernel<64>, items, 256, F32Cfg<64>::SMEM, s, o, a);
+    default: return launch_packed(packed_f32_kernel<128>, items, 256, F32Cfg<128>::SMEM, s, o, a);
   }
 }
 

@@ -232,7 +232,7 @@ __device__ __forceinline__ uint32_t codes8(const Raw8<T> &x, float m, float s) {
 }
 
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(256) kv4_store_kernel(RowArgs a) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) kv4_store_kernel(RowArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ int scu[CU_SMEM + 1];
