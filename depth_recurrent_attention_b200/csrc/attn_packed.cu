@@ -790,23 +790,10 @@ bool row_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, lon
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename K, typename... A>
-int launch_packed(K kern, long items, int threads, int smem, cudaStream_t s, LaunchOpt o, const A &...args) {
+template <auto KERN, typename... A>
+int launch_items(long items, int threads, int smem, cudaStream_t s, LaunchOpt o, const A &...args) {
   if (items > 0x7fffffffL) return DREAMER_ERR_UNSUPPORTED;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return DREAMER_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)items);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = o.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DREAMER_OK : DREAMER_ERR_CUDA;
+  return launch<KERN>(dim3((unsigned)items), dim3(threads), smem, 1, s, o, args...);
 }
 
 // the most row tiles that n_tokens rows in n_seq prompts can make
@@ -832,15 +819,15 @@ int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
         !row_map(&tv, p.v, (uint64_t)p.Hkv * p.d, p.n_tokens, p.ldv))
       return DREAMER_ERR_CUDA;
     const long items = most_tiles(p.n_tokens, p.n_seq, 256) * p.Hq;
-    if (p.d == 64) return launch_packed(packed_tc_kernel<64>, items, 352, PkCfg<64>::SMEM, s, o, tq, tk, tv, a);
-    return launch_packed(packed_tc_kernel<128>, items, 352, PkCfg<128>::SMEM, s, o, tq, tk, tv, a);
+    if (p.d == 64) return launch_items<packed_tc_kernel<64>>(items, 352, PkCfg<64>::SMEM, s, o, tq, tk, tv, a);
+    return launch_items<packed_tc_kernel<128>>(items, 352, PkCfg<128>::SMEM, s, o, tq, tk, tv, a);
   }
   const long items = most_tiles(p.n_tokens, p.n_seq, 32) * p.Hq;
   switch (p.d) {
-    case 16: return launch_packed(packed_f32_kernel<16>, items, 256, F32Cfg<16>::SMEM, s, o, a);
-    case 32: return launch_packed(packed_f32_kernel<32>, items, 256, F32Cfg<32>::SMEM, s, o, a);
-    case 64: return launch_packed(packed_f32_kernel<64>, items, 256, F32Cfg<64>::SMEM, s, o, a);
-    default: return launch_packed(packed_f32_kernel<128>, items, 256, F32Cfg<128>::SMEM, s, o, a);
+    case 16: return launch_items<packed_f32_kernel<16>>(items, 256, F32Cfg<16>::SMEM, s, o, a);
+    case 32: return launch_items<packed_f32_kernel<32>>(items, 256, F32Cfg<32>::SMEM, s, o, a);
+    case 64: return launch_items<packed_f32_kernel<64>>(items, 256, F32Cfg<64>::SMEM, s, o, a);
+    default: return launch_items<packed_f32_kernel<128>>(items, 256, F32Cfg<128>::SMEM, s, o, a);
   }
 }
 

@@ -1327,38 +1327,6 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a, int share) {
   for (int c = 0; c < C; c++) dst[C * lane + c] = from_f<T>(nb ? acc[c] * inv : 0.f);
 }
 
-template <typename K, typename... A>
-int launch(K kern, dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s, LaunchOpt o, A... args) {
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return DREAMER_ERR_CUDA;
-  if (cluster > 8 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return DREAMER_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  int na = 0;
-  if (o.pdl) {
-    at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[na].val.programmaticStreamSerializationAllowed = 1;
-    na++;
-  }
-  if (cluster > 1) {
-    at[na].id = cudaLaunchAttributeClusterDimension;
-    at[na].val.clusterDim.x = cluster;
-    at[na].val.clusterDim.y = 1;
-    at[na].val.clusterDim.z = 1;
-    na++;
-  }
-  cfg.attrs = at;
-  cfg.numAttrs = na;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DREAMER_OK : DREAMER_ERR_CUDA;
-}
-
 RowArgs row_args(const Kv4Cache &c, const Kv4Rows &r) {
   RowArgs a{};
   a.data = c.data;
@@ -1407,24 +1375,24 @@ int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
     using C = SplitCfg<T, NG>;
     const int grid = device_sms() * C::OCC;
     a.n_warps = grid * C::NW;
-    const int rc = launch(kv4_split_kernel<T, NG, GP, C::NW, C::ST, C::OCC>, dim3(grid), dim3(C::NW * 32),
-                          C::NW * C::ST * W::BLK, 1, s, o, a);
+    const int rc = launch<kv4_split_kernel<T, NG, GP, C::NW, C::ST, C::OCC>>(dim3(grid), dim3(C::NW * 32),
+                                                                             C::NW * C::ST * W::BLK, 1, s, o, a);
     if (rc) return rc;
     LaunchOpt j;
     j.pdl = true;  // the split kernel precedes it on the stream
     // warps a query head: one for each four of the slots that items have on average
     const long outs = (long)a.B * a.Hkv * a.G, mean = a.n_warps / items;
     const int share = mean > 64 ? 8 : mean > 32 ? 4 : mean > 8 ? 2 : 1;
-    return launch(kv4_join_kernel<T, W::D, GP, C::NW>, dim3((unsigned)((outs * share + 7) / 8)), dim3(256), 0, 1, s, j, a,
-                  share);
+    return launch<kv4_join_kernel<T, W::D, GP, C::NW>>(dim3((unsigned)((outs * share + 7) / 8)), dim3(256), 0, 1, s, j, a,
+                                                       share);
   }
   constexpr int NW = 4, ST = 3;
   // CTAs of an item: at least a block a warp, and no more than fill the GPU
   int cluster = 1;
   while (cluster < 8 && items * cluster < 148 * 2 && nblk > NW * cluster) cluster *= 2;
   constexpr int part = NW * GP * W::D * 4, rings = NW * ST * W::BLK;
-  return launch(kv4_attn_kernel<T, NG, GP, NW, ST>, dim3((unsigned)(items * cluster)), dim3(NW * 32),
-                rings > part ? rings : part, cluster, s, o, a);
+  return launch<kv4_attn_kernel<T, NG, GP, NW, ST>>(dim3((unsigned)(items * cluster)), dim3(NW * 32),
+                                                    rings > part ? rings : part, cluster, s, o, a);
 }
 
 template <typename T, int NG>
@@ -1441,19 +1409,29 @@ int dispatch_attn(const AttnArgs &a, cudaStream_t s, LaunchOpt o) {
 int kv4_store(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o) {
   if (r.n_rows == 0) return DREAMER_OK;
   const RowArgs a = row_args(c, r);
-  const bool many = many_rows(a);
-  auto go = [&](void (*kern)(RowArgs)) { return launch(kern, row_grid(a, many ? 64 : 16), dim3(256), 0, 1, s, o, a); };
-  if (r.dtype == 0) return go(many ? kv4_store_kernel<float, 64> : kv4_store_kernel<float, 16>);
-  return go(many ? kv4_store_kernel<bf16, 64> : kv4_store_kernel<bf16, 16>);
+  const bool f32 = r.dtype == 0;
+  if (many_rows(a)) {
+    const dim3 g = row_grid(a, 64);
+    return f32 ? launch<kv4_store_kernel<float, 64>>(g, dim3(256), 0, 1, s, o, a)
+               : launch<kv4_store_kernel<bf16, 64>>(g, dim3(256), 0, 1, s, o, a);
+  }
+  const dim3 g = row_grid(a, 16);
+  return f32 ? launch<kv4_store_kernel<float, 16>>(g, dim3(256), 0, 1, s, o, a)
+             : launch<kv4_store_kernel<bf16, 16>>(g, dim3(256), 0, 1, s, o, a);
 }
 
 int kv4_load(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o) {
   if (r.n_rows == 0) return DREAMER_OK;
   const RowArgs a = row_args(c, r);
-  const bool many = many_rows(a);
-  auto go = [&](void (*kern)(RowArgs)) { return launch(kern, row_grid(a, many ? 64 : 16), dim3(256), 0, 1, s, o, a); };
-  if (r.dtype == 0) return go(many ? kv4_load_kernel<float, 64> : kv4_load_kernel<float, 16>);
-  return go(many ? kv4_load_kernel<bf16, 64> : kv4_load_kernel<bf16, 16>);
+  const bool f32 = r.dtype == 0;
+  if (many_rows(a)) {
+    const dim3 g = row_grid(a, 64);
+    return f32 ? launch<kv4_load_kernel<float, 64>>(g, dim3(256), 0, 1, s, o, a)
+               : launch<kv4_load_kernel<bf16, 64>>(g, dim3(256), 0, 1, s, o, a);
+  }
+  const dim3 g = row_grid(a, 16);
+  return f32 ? launch<kv4_load_kernel<float, 16>>(g, dim3(256), 0, 1, s, o, a)
+             : launch<kv4_load_kernel<bf16, 16>>(g, dim3(256), 0, 1, s, o, a);
 }
 
 int kv4_attn(const Kv4Cache &c, const Kv4Attn &t, cudaStream_t s, LaunchOpt o) {

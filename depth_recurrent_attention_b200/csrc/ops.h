@@ -5,6 +5,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "../../include/dreamer.h"
+
 namespace dreamer {
 namespace ops {
 
@@ -13,6 +17,54 @@ namespace ops {
 struct LaunchOpt {
   bool pdl = false;
 };
+
+// Launch of one kernel (a template argument, so that what is noted of it is its own).  Its limit of
+// dynamic shared memory is raised once a device, noted in bit d of `raised`, and again where a launch
+// is refused all the same (a context that was reset has lost it).
+template <auto KERN, typename... A>
+int launch(dim3 grid, dim3 block, int smem, int cluster, cudaStream_t s, LaunchOpt o, const A &...args) {
+  static std::atomic<unsigned long long> raised{0};
+  const bool large = smem > 48 * 1024;
+  for (bool again = false;; again = true) {
+    if (large) {
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess) return DREAMER_ERR_CUDA;
+      const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+      if (again || !(raised.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+          cudaGetLastError();
+          return DREAMER_ERR_CUDA;
+        }
+        raised.fetch_or(bit, std::memory_order_release);
+      }
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    int na = 0;
+    if (o.pdl) {
+      at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[na].val.programmaticStreamSerializationAllowed = 1;
+      na++;
+    }
+    if (cluster > 1) {
+      at[na].id = cudaLaunchAttributeClusterDimension;
+      at[na].val.clusterDim.x = cluster;
+      at[na].val.clusterDim.y = 1;
+      at[na].val.clusterDim.z = 1;
+      na++;
+    }
+    cfg.attrs = at;
+    cfg.numAttrs = na;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, KERN, args...);
+    if (e == cudaSuccess) return DREAMER_OK;
+    cudaGetLastError();
+    if (again || !large || e != cudaErrorInvalidValue) return DREAMER_ERR_CUDA;
+  }
+}
 
 // ---- causal attention over packed prompts -------------------------------------------------
 struct PackedAttn {
