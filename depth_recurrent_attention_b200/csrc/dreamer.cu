@@ -1020,7 +1020,7 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
       if (ops::kv4_store(c4, r4, st, o) != DREAMER_OK) h->path_err = 1;
       o.pdl = pdl_take(h, st);
       if (ops::kv4_attn(c4, a4, st, o) != DREAMER_OK) h->path_err = 1;
-      g_launches += ops::kv4_attn_workspace(c4, c.n_heads) ? 3 : 2;
+      g_launches += 1 + ops::kv4_attn_launches(c4, c.n_heads, c.dtype);
       return;
     }
     if (io.mode == 3) {

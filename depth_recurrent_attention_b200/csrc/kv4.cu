@@ -892,7 +892,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
-// Form for little work (one launch): a cluster of CTAs takes one (sequence, key head, chunk of GP
+// Cluster form (one launch): a cluster of CTAs takes one (sequence, key head, chunk of GP
 // query heads), every CTA a contiguous share of its blocks, every warp each NW-th block of that;
 // warps join in shared memory, CTAs in distributed shared memory.
 template <typename T, int NG, int GP, int NW, int ST>
@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
   if (csize > 1) cluster_sync();  // shared memory that others read stays until they have
 }
 
-// Form for much work: the blocks of all items (sequence, key head, chunk of query heads) form one
+// Split form: the blocks of all items (sequence, key head, chunk of query heads) form one
 // sequence, item by item, and every warp of a grid that fills the GPU once takes an equal run of it,
 // whatever the lengths.  A warp that holds a whole item writes its output; the others leave
 // partial outputs in slot (warp + item), and kv4_join_kernel joins an item's slots, which are
@@ -1352,8 +1352,8 @@ int device_sms() {
   return sms;
 }
 
-// Warps a CTA, ring stages and CTAs an SM of the split form
-template <typename T, int NG> struct SplitCfg {
+// Warps a CTA, ring stages and CTAs an SM (a third stage, or a fifth CTA, measured no faster)
+template <typename T, int NG> struct FormCfg {
   static constexpr int NW = 4;
   static constexpr int ST = NG == 1 ? 3 : 2;
   static constexpr int OCC = sizeof(T) == 4 ? 2 : NG == 1 ? 4 : 3;
@@ -1361,8 +1361,22 @@ template <typename T, int NG> struct SplitCfg {
 
 int heads_a_chunk(int G) { return G <= 2 ? 2 : G <= 4 ? 4 : 8; }
 
-// The split form pays where one cluster launch would leave warps with several blocks each
-bool use_split(long items, int nblk) { return items * nblk > 4096; }
+// How the items are spread over the GPU's `slots` CTAs, from the number of items and the most blocks
+// of one (the lengths are known on the device only).  A cluster form's CTAs join by themselves, the
+// hardware hands out what does not fit at once, and equal lengths keep every warp busy: 1024 items of
+// 4096 tokens, head dim 64, 52 us against 59 of the split form.  The split form pays a second launch and
+// evens out what a single wave cannot: items fewer than slots with long runs of blocks a warp (4
+// items of 131071 tokens, head dim 128, 86 -> 27 us; 128 of 1 to 8192 tokens 31 -> 21, all of 8192 37 -> 38).
+struct Plan {
+  int cluster;
+  bool split;
+};
+Plan plan_for(long items, int nblk, long slots, int nw) {
+  Plan p{1, false};
+  while (p.cluster < 8 && items * p.cluster * 2 <= slots && nblk > nw * p.cluster) p.cluster *= 2;
+  p.split = items * p.cluster <= slots && nblk >= nw * p.cluster * (p.cluster == 8 ? 6 : 12);
+  return p;
+}
 
 template <typename T, int NG, int GP>
 int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
@@ -1371,9 +1385,11 @@ int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
   const long items = (long)a.B * a.Hkv * a.qchunks;
   const int nblk = a.cap / KV4_BLOCK;
   if (items * (nblk + ITEM_COST) >= 0x7fffffffL) return DREAMER_ERR_UNSUPPORTED;
-  if (use_split(items, nblk)) {
-    using C = SplitCfg<T, NG>;
-    const int grid = device_sms() * C::OCC;
+  using C = FormCfg<T, NG>;
+  const int sms = device_sms();
+  const Plan p = plan_for(items, nblk, (long)sms * C::OCC, C::NW);
+  if (p.split) {
+    const int grid = sms * C::OCC;
     a.n_warps = grid * C::NW;
     const int rc = launch<kv4_split_kernel<T, NG, GP, C::NW, C::ST, C::OCC>>(dim3(grid), dim3(C::NW * 32),
                                                                              C::NW * C::ST * W::BLK, 1, s, o, a);
@@ -1386,13 +1402,9 @@ int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
     return launch<kv4_join_kernel<T, W::D, GP, C::NW>>(dim3((unsigned)((outs * share + 7) / 8)), dim3(256), 0, 1, s, j, a,
                                                        share);
   }
-  constexpr int NW = 4, ST = 3;
-  // CTAs of an item: at least a block a warp, and no more than fill the GPU
-  int cluster = 1;
-  while (cluster < 8 && items * cluster < 148 * 2 && nblk > NW * cluster) cluster *= 2;
-  constexpr int part = NW * GP * W::D * 4, rings = NW * ST * W::BLK;
-  return launch<kv4_attn_kernel<T, NG, GP, NW, ST>>(dim3((unsigned)(items * cluster)), dim3(NW * 32),
-                                                    rings > part ? rings : part, cluster, s, o, a);
+  constexpr int part = C::NW * GP * W::D * 4, rings = C::NW * C::ST * W::BLK;
+  return launch<kv4_attn_kernel<T, NG, GP, C::NW, C::ST>>(dim3((unsigned)(items * p.cluster)), dim3(C::NW * 32),
+                                                          rings > part ? rings : part, p.cluster, s, o, a);
 }
 
 template <typename T, int NG>
@@ -1447,11 +1459,22 @@ int kv4_attn(const Kv4Cache &c, const Kv4Attn &t, cudaStream_t s, LaunchOpt o) {
   return t.dtype == 0 ? dispatch_attn<float, 2>(a, s, o) : dispatch_attn<bf16, 2>(a, s, o);
 }
 
+int kv4_attn_launches(const Kv4Cache &c, int Hq, int dtype) {
+  const int G = Hq / c.Hkv, gp = heads_a_chunk(G);
+  const long items = (long)c.B * c.Hkv * ((G + gp - 1) / gp);
+  const int occ = dtype == 0 ? FormCfg<float, 1>::OCC : c.d == 64 ? FormCfg<bf16, 1>::OCC : FormCfg<bf16, 2>::OCC;
+  return plan_for(items, c.cap / KV4_BLOCK, (long)device_sms() * occ, 4).split ? 2 : 1;
+}
+
 long kv4_attn_workspace(const Kv4Cache &c, int Hq, bool any_capacity) {
   const int G = Hq / c.Hkv, gp = heads_a_chunk(G);
   const long items = (long)c.B * c.Hkv * ((G + gp - 1) / gp);
-  if (!any_capacity && !use_split(items, c.cap / KV4_BLOCK)) return 0;
-  const long warps = (long)device_sms() * 16;  // of either type
+  const int nblk = c.cap / KV4_BLOCK, sms = device_sms();
+  const int occ = c.d == 64 ? FormCfg<bf16, 1>::OCC : FormCfg<bf16, 2>::OCC;
+  if (!any_capacity && !plan_for(items, nblk, (long)sms * occ, 4).split &&
+      !plan_for(items, nblk, (long)sms * FormCfg<float, 1>::OCC, 4).split)
+    return 0;
+  const long warps = (long)sms * 16;  // of either type
   return (warps + items) * gp * (c.d + 4) * (long)sizeof(float);
 }
 

@@ -125,6 +125,7 @@ struct Kv4Attn {
 };
 // bytes of the workspace (0: none needed); any_capacity: whatever c.cap is
 long kv4_attn_workspace(const Kv4Cache &c, int Hq, bool any_capacity = false);
+int kv4_attn_launches(const Kv4Cache &c, int Hq, int dtype);  // kernels of a call
 int kv4_attn(const Kv4Cache &c, const Kv4Attn &a, cudaStream_t s, LaunchOpt o = LaunchOpt());
 
 }  // namespace ops

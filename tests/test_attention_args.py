@@ -117,7 +117,7 @@ def test_the_packed_binding_refuses_tensors_of_the_host():
 
 
 def test_workspace_of_attention(L):
-    small, large = _cache(), _cache(batch=64, n_kv_heads=16, capacity=8192)
+    small, large = _cache(), _cache(batch=2, n_kv_heads=2, capacity=1 << 15)
     assert L.dreamer_attn_kv4_workspace(small, 4) == 0
     need = L.dreamer_attn_kv4_workspace(large, 16)
     assert need > 0 and L.dreamer_attn_kv4_workspace(large, 17) == 0 and L.dreamer_attn_kv4_workspace(None, 16) == 0

@@ -159,6 +159,7 @@ def _cache(rng, lens, H, d, cap, dtype="bf16"):
     return c
 
 
+@pytest.mark.parametrize("capacity", [0, 13000])   # as much as is needed; enough for runs over all items
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lens,H,G,d", [
     ([1], 1, 1, 64),
@@ -172,9 +173,9 @@ def _cache(rng, lens, H, d, cap, dtype="bf16"):
     ([3000, 1500], 1, 1, 128),                          # split over a cluster
     ([5000], 1, 2, 64),
 ])
-def test_attend_against_64_bits(cuda, dtype, lens, H, G, d):
+def test_attend_against_64_bits(cuda, dtype, lens, H, G, d, capacity):
     rng = np.random.default_rng(sum(lens) + H * G)
-    c = _cache(rng, lens, H, d, max(lens) + 1)
+    c = _cache(rng, lens, H, d, max(capacity, max(lens) + 1))
     q = _t(rng.standard_normal((len(lens), H * G, d)) * 2, dtype)
     out = c.attend(q, _ints(lens))
     ref, tol = R.attend(c.data[0].cpu().numpy(), d, _f64(q), lens, d ** -0.5, EPS[dtype])
@@ -182,19 +183,21 @@ def test_attend_against_64_bits(cuda, dtype, lens, H, G, d):
     assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
 
 
-def test_attend_does_not_use_what_lies_behind_the_last_key(cuda):
+@pytest.mark.parametrize("capacity", [192, 192 * 70])
+def test_attend_does_not_use_what_lies_behind_the_last_key(cuda, capacity):
     """NaN pairs and random codes behind lens[b] change no bit."""
     import torch
     rng = np.random.default_rng(11)
     lens = [70, 64, 1, 0]
-    c = _cache(rng, [130] * 4, 2, 128, 192)
+    c = _cache(rng, [130] * 4, 2, 128, capacity)
     q = _t(rng.standard_normal((4, 4, 128)), "bf16")
     a = c.attend(q, _ints(lens))
-    pos = torch.arange(192, device="cuda").view(3, 64)
-    plane = c.data[0].view(4, 2, 3, -1)
-    pairs = plane[..., 4 * 64 * 32:].view(torch.int16).view(4, 2, 3, 4, 64, 2)
+    nb = capacity // 64
+    pos = torch.arange(capacity, device="cuda").view(nb, 64)
+    plane = c.data[0].view(4, 2, nb, -1)
+    pairs = plane[..., 4 * 64 * 32:].view(torch.int16).view(4, 2, nb, 4, 64, 2)
     for b, n in enumerate(lens):
-        hid = (pos >= n)[None, :, None, :, None].expand(2, 3, 4, 64, 2)
+        hid = (pos >= n)[None, :, None, :, None].expand(2, nb, 4, 64, 2)
         pairs[b][hid] = 0x7FC0
     b_ = c.attend(q, _ints(lens))
     assert torch.equal(a, b_) and (b_[3] == 0).all()
@@ -220,13 +223,14 @@ def test_attend_of_nan_keys_and_large_scores(cuda):
     assert (np.abs(_f64(big) - ref) <= tol).all()
 
 
-def test_attend_strides_streams_graphs_and_repeatability(cuda):
+@pytest.mark.parametrize("capacity", [2048, 16384])
+def test_attend_strides_streams_graphs_and_repeatability(cuda, capacity):
     """q as a slice of a wider row, out in place of q, another stream, a captured and replayed
     graph whose lengths change between replays: the same bits as the plain call."""
     import torch
     rng = np.random.default_rng(13)
     lens = [2000, 700, 64]
-    c = _cache(rng, lens, 2, 64, 2048)
+    c = _cache(rng, lens, 2, 64, capacity)
     wide = _t(rng.standard_normal((3, 12, 64)), "bf16")
     q = wide[:, 4:8]
     ln = _ints(lens)
@@ -250,15 +254,16 @@ def test_attend_strides_streams_graphs_and_repeatability(cuda):
         assert torch.equal(out, c.attend(q, _ints(cut)))
 
 
-def test_attend_reports_lengths_outside_the_cache(cuda):
+@pytest.mark.parametrize("capacity", [64, 64 * 200])
+def test_attend_reports_lengths_outside_the_cache(cuda, capacity):
     import torch
     rng = np.random.default_rng(14)
-    c = _cache(rng, [60, 60], 1, 64, 64)
+    c = _cache(rng, [60, 60], 1, 64, capacity)
     q = _t(rng.standard_normal((2, 1, 64)), "bf16")
     st = _ints([0])
     good = c.attend(q, _ints([60, 64]), status=st)
     assert st.item() == 0
-    for bad in (65, -1, 2 ** 31 - 1):
+    for bad in (capacity + 1, -1, 2 ** 31 - 1):
         st.zero_()
         o = c.attend(q, _ints([60, bad]), status=st)
         assert st.item() != 0 and torch.equal(o[0], good[0]) and (o[1] == 0).all()
@@ -278,3 +283,37 @@ def test_offsets_past_32_bits(cuda):
     c.store(k, v, cu, _ints([0, 0, 0, at]))
     a, b = c.load(cu, _ints([0, 0, 0, at]), n, torch.float32)
     assert np.array_equal(_f64(a), R.held(_f64(k))) and np.array_equal(_f64(b), R.held(_f64(v)))
+
+
+def test_attend_over_many_items_and_long_runs(cuda):
+    """More query heads than a chunk, sequences from none to several CTAs' runs: each head equals the
+    same head attended with the others' sequences emptied (the runs then lie elsewhere) to rounding."""
+    import torch
+    rng = np.random.default_rng(16)
+    lens = [0, 12800, 1, 7000, 0, 65, 300, 9999]
+    c = _cache(rng, lens, 2, 128, 12800)
+    q = _t(rng.standard_normal((8, 22, 128)), "fp32")
+    a = c.attend(q, _ints(lens))
+    assert (a[0] == 0).all() and (a[4] == 0).all()
+    for b in (1, 3, 5, 7):
+        only = [n if i == b else 0 for i, n in enumerate(lens)]
+        o = c.attend(q, _ints(only))
+        # the order of float32 sums over n keys: n 2^-23 of the sum of magnitudes, here below 64 |v|
+        assert (o[b] - a[b]).abs().max() <= lens[b] * 2.0 ** -23 * 64
+        assert (o[[i for i in range(8) if i != b]] == 0).all()
+
+
+def test_two_streams_attend_at_once(cuda):
+    """Each call has a workspace of its own."""
+    import torch
+    rng = np.random.default_rng(17)
+    cs = [_cache(rng, [9000, 100], 2, 64, 13000) for _ in range(2)]
+    q = _t(rng.standard_normal((2, 4, 64)), "bf16")
+    ln = _ints([9000, 100])
+    want = [c.attend(q, ln) for c in cs]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [c.attend(q, ln, stream=s) for c, s in zip(cs, ss)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
