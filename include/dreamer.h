@@ -240,7 +240,7 @@ int dreamer_attn_packed(const void *q, int64_t ldq, const void *k, int64_t ldk, 
  * These entry points need no handle and allocate nothing.  A group is 64 consecutive channels
  * of one head of one token: s = (max - min) / 15 and m = min, both rounded to bfloat16,
  * c = round((x - m) / s) in 0..15 (half to even; 0 where s = 0); the value held is s c + m.
- * A group with a NaN, an infinity or a magnitude above 2^126 is held, and read back, as NaN.
+ * A group with a NaN, an infinity or a magnitude above 2^100 is held, and read back, as NaN.
  *
  * `data` holds one depth: [batch][n_kv_heads][capacity / 64] blocks of 64 tokens, a block being
  * K codes [head_dim / 64][64][32 bytes] (channel 2i in the low half of byte i), V codes
@@ -281,9 +281,10 @@ int dreamer_kv4_load(const dreamer_kv4_cache *cache, void *k, int64_t ldk, void 
  * sequence b attends positions 0 .. lens[b]-1 of key head j / (n_heads / n_kv_heads),
  *   out = sum_i softmax_i(scale q . k_i) v_i,
  * and a sequence with lens[b] = 0 gets zeros.  q, out: [batch] rows of n_heads * head_dim of
- * dtype (out may be q); lens [batch] int32; n_heads a multiple of n_kv_heads.  Sums, softmax
- * and products are float32, the weights of the output product bfloat16 for bfloat16 (float32
- * in three terms for float32).  What lies in the cache behind lens[b] is not used.
+ * dtype (out may be q); lens [batch] int32; n_heads a multiple of n_kv_heads.  Sums and softmax
+ * are float32; bfloat16 takes q, and a 64-token block's weights, as 16-bit fixed-point numbers of
+ * their largest (of 64 channels; of the block), float32 works to float32 precision throughout.
+ * What lies in the cache behind lens[b] is not used.
  * workspace: device memory of at least dreamer_attn_kv4_workspace() bytes (NULL where that is 0),
  * 16-byte aligned, contents of no matter; calls that may run at the same time need one each.  */
 int dreamer_attn_kv4(const dreamer_kv4_cache *cache, const void *q, int64_t ldq, void *out,

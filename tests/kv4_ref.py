@@ -2,7 +2,7 @@
 
 A group is 64 channels: s = (max - min) / 15 and m = min, both rounded to bf16 (through
 float32), c = rint((x - m) / s) in 0..15 (0 where s = 0), value s c + m; a group with a NaN or a
-magnitude above 2^126 holds NaN.  A block is 64 tokens: K codes [ng][64][32 bytes] (channel 2i
+magnitude above 2^100 holds NaN.  A block is 64 tokens: K codes [ng][64][32 bytes] (channel 2i
 low), V codes, K pairs [ng][64][2] bf16, V pairs.
 """
 import numpy as np
@@ -24,7 +24,7 @@ def quantise(x):
     """x [..., d] float64 -> (codes [..., ng, 64] int, s, m [..., ng] float64)."""
     x = np.asarray(x, np.float64)
     x = x.reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
-    bad = ~(np.abs(x) <= 2.0 ** 126).all(-1)
+    bad = ~(np.abs(x) <= 2.0 ** 100).all(-1)
     x = np.where(bad[..., None], 0.0, x)
     s = bf16((x.max(-1) - x.min(-1)) / 15.0)
     m = bf16(x.min(-1))

@@ -77,7 +77,7 @@ def test_quotients_next_to_a_half_and_constant_groups(cuda):
     from depth_recurrent_attention_b200.attention import KV4Cache
     rng = np.random.default_rng(5)
     rows = []
-    for s in (1.0, 0.3330078125, 2.0 ** -100, 3e-39, 1e36, 7.0):
+    for s in (1.0, 0.3330078125, 2.0 ** -100, 3e-39, 1e28, 7.0):
         s = float(R.bf16([s])[0])
         x = np.float32(s) * (rng.integers(0, 15, 64) + 0.5).astype(np.float32)
         x = np.nextafter(x, np.where(np.arange(64) % 3 == 0, np.inf, np.where(np.arange(64) % 3 == 1, -np.inf, x)).astype(np.float32))

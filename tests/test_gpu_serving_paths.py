@@ -46,6 +46,10 @@ FREE = dict(n_experts=4, top_k=4)
     ("small", [1, 129, 0, 200, 77], dict(depth=3, **FREE)),
     ("small", [300, 100], dict(depth=3, n_proj_experts=1, **FREE)),          # grouped projections
     ("small", [130, 2, 250], dict(depth=2, n_heads=4, head_dim=128, **FREE)),
+    ("small", [150, 77], dict(depth=2, variant=1, n_proj_experts=1, **FREE)),  # serial layout, rows gathered
+    ("small", [150, 77], dict(depth=2, variant=2, **FREE)),
+    ("small", [150, 77], dict(depth=2, variant=3, n_proj_experts=1, **FREE)),
+    ("small", [150, 77], dict(depth=3, da_window=2, **FREE)),
     ("small", [1], dict(depth=2, **FREE)),
     ("small", [64, 65], dict(depth=2, dtype="fp32", n_experts=16, top_k=2)),
 ])
@@ -75,8 +79,14 @@ def test_packed_forward_equals_each_prompt_alone(cuda, base, lens, kw):
                 _, flips = PY.check_routing(one, W, l, tr["idx"][l, a:e].cpu().numpy(), r["idx"][l],
                                             r["margin"][l], strict=True)
                 assert flips == 0
+            # The serial layout's sequence attention reads u = x^ + DA W_O rounded to bf16, half a step of
+            # 2^-8 |u|.  With projection experts the absorbed weights have twice the variance, |u| reaches
+            # 8 and its rounding 2^-6 = 1.6e-2 an element; W_QKV and W_O (each of gain sqrt 2 in rms) double
+            # that to 3.1e-2 before any other rounding: the absolute bound of 3e-2 says nothing there, for
+            # the equal-length forward as little (its states are the same bits, below).
+            loose = cfg.variant == 1 and cfg.n_proj_experts > 0
             PY.check_drift(PY.to_np(tr["y"][l, a:e]), r["y"][l], f"y depth {l} rows {a}..{e}",
-                           gate_abs=l == 0 and bf, f32=PY.to_np(tr["y_f32"][l, a:e]))
+                           gate_abs=l == 0 and bf and not loose, f32=PY.to_np(tr["y_f32"][l, a:e]))
             PY.check_drift(PY.to_np(tr["sa_k"][l, a:e]), r["sa_k"][l], f"k depth {l}", gate_abs=False)
             PY.check_drift(PY.to_np(tr["sa_v"][l, a:e]), r["sa_v"][l], f"v depth {l}", gate_abs=False)
         if bf:
@@ -90,6 +100,23 @@ def test_packed_forward_equals_each_prompt_alone(cuda, base, lens, kw):
         o.zero_()
         dev.forward_packed(x, c, x_out=o)
         assert torch.equal(o, out)
+    dev.close()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(variant=1), dict(variant=1, n_proj_experts=1), dict(variant=2),
+                                dict(variant=3), dict(n_proj_experts=1), dict(n_heads=4, head_dim=128)])
+def test_packed_equal_prompts_are_the_equal_length_forward(cuda, kw):
+    import torch
+    cfg = configs.SMALL.with_(batch=2, seq=256, depth=2, **{**FREE, **kw})
+    W = inputs.host_weights(cfg)
+    dev = _handle(cfg, W)
+    x = inputs.to_device(inputs.extra_normal(cfg, 5003, (cfg.tokens, cfg.hidden), 1.0), "bf16")
+    a = {n: t for n, t in _trace(cfg, cfg.tokens, ["y_f32"]).items()}
+    b = {n: t for n, t in _trace(cfg, cfg.tokens, ["y_f32"]).items()}
+    dev.forward(x, trace=a)
+    dev.forward_packed(x, _ints([0, 256, 512]), trace=b)
+    # the same arithmetic in the same order but for the sums inside the attention kernels
+    assert PY.rel_l2(PY.to_np(b["y_f32"][0]), PY.to_np(a["y_f32"][0])) <= 1e-3
     dev.close()
 
 
@@ -139,13 +166,15 @@ def _caches(cfg, lens, seed):
     ([130, 64, 5], dict(variant=3, dtype="fp32")),
     ([130, 64, 5], dict(da_window=1, dtype="fp32", n_heads=4, head_dim=128)),
     ([(7 * i) % 61 for i in range(70)], dict(da_window=1)),
+    ([40, 0, 17], dict(da_window=1, n_proj_experts=1)),
+    ([13000, 5], dict(variant=3, depth=1)),               # long caches: runs over all items
 ])
 def test_decode_step_over_4_bit_caches(cuda, lens, kw):
     """Every depth against its own x^ (traced): the new key and value are in the cache within half
     a step, and y = x^ + W_O [SA over what the cache holds | DA], where a window of one depth makes
     DA the depth's own value."""
     import torch
-    cfg = configs.SMALL.with_(batch=len(lens), seq=1, depth=3, cache_len=max(lens) + 1, **{**FREE, **kw})
+    cfg = configs.SMALL.with_(**{**dict(batch=len(lens), seq=1, depth=3, cache_len=max(lens) + 1), **FREE, **kw})
     B, h, d, H = cfg.batch, cfg.hidden, cfg.head_dim, cfg.n_heads
     W = inputs.host_weights(cfg)
     dev = _handle(cfg, W)
@@ -153,15 +182,17 @@ def test_decode_step_over_4_bit_caches(cuda, lens, kw):
     before = c.data.clone()
     x = inputs.to_device(inputs.extra_normal(cfg, 6100, (B, h), 1.0), cfg.dtype)
     ln = _ints(lens)
-    tr = _trace(cfg, B, ["xhat", "y", "y_f32"])
+    tr = _trace(cfg, B, ["xhat", "y", "y_f32"] + (["psig"] if cfg.n_proj_experts else []))
     out = dev.decode_step_kv4(x, c, ln, trace=tr)
     dev.route_counts()                                   # no device error
     assert torch.isfinite(out).all()
     bf = cfg.dtype == "bf16"
-    wq, wo = W["w_qkv"][0].astype(np.float64), W["w_o"][0].astype(np.float64)
+    D = PY.deployed_weights(cfg, W)
+    wq, wo = D["w_qkv"][0].astype(np.float64), D["w_o"][0].astype(np.float64)
     for l in range(cfg.depth):
         xh = PY.to_np(tr["xhat"][l])
-        qkv = xh @ wq
+        sig = PY.to_np(tr["psig"][l])[:, None] if cfg.n_proj_experts else 1.0   # one projection expert
+        qkv = sig * (xh @ wq)
         q, k, v = (qkv[:, i * h:(i + 1) * h].reshape(B, H, d) for i in range(3))
         q = np.stack([[O.rope(q[b, j], lens[b]) for j in range(H)] for b in range(B)])
         k = np.stack([[O.rope(k[b, j], lens[b]) for j in range(H)] for b in range(B)])
@@ -174,7 +205,7 @@ def test_decode_step_over_4_bit_caches(cuda, lens, kw):
             assert (np.abs(got.reshape(g.shape) - g) <= tol[..., None]).all()
         att, _ = R.attend(c.data[l].cpu().numpy(), d, q, [n + 1 for n in lens], d ** -0.5, 0.0)
         da = qkv[:, 5 * h:] if cfg.variant != 3 else np.zeros((B, h))
-        y = xh + np.concatenate([att.reshape(B, h), da], 1) @ wo
+        y = xh + sig * (np.concatenate([att.reshape(B, h), da], 1) @ wo)
         PY.check_hidden(PY.to_np(tr["y"][l]), y, bf, f"y depth {l}", f32=PY.to_np(tr["y_f32"][l]) if bf else None)
     # nothing but the new positions changed
     pos = torch.arange(c.capacity, device="cuda")
