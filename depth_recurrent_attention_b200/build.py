@@ -1,6 +1,6 @@
-"""Build libdreamer.so (the product), libdreamer_inputs.so (seeded input generator) and
-libdreamer_testhooks.so (test infrastructure: the product's sources with the timeout-test hook
-and a 20 ms device wait limit) for sm_100a with nvcc, in-tree."""
+"""Build libdreamer.so (the product), _attention.so (its Python entry points of attention.py),
+libdreamer_inputs.so (seeded input generator) and libdreamer_testhooks.so (test infrastructure:
+the product's sources with the timeout-test hook and a 20 ms device wait limit) for sm_100a, in-tree."""
 import os
 import subprocess
 import sys
@@ -9,6 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+CUDA = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 # translation units of libdreamer.so
 UNITS = ("dreamer.cu", "route_noalloc.cu", "attn_packed.cu", "kv4.cu")
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -22,6 +23,28 @@ def _newer(target, deps):
         return False
     t = os.path.getmtime(target)
     return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def _build_attention(libdreamer, force, verbose):
+    """_attention: the Python entry points of attention.py, over libdreamer.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    out = os.path.join(HERE, "_attention.so")
+    src = os.path.join(CSRC, "attention_py.cpp")
+    if not force and _newer(out, [src, libdreamer]):
+        return out
+    inc = [*ext.include_paths(), sysconfig.get_paths()["include"], os.path.join(CUDA, "include")]
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unused-local-typedefs",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{p}" for p in inc), "-o", out, src, f"-L{HERE}", "-l:libdreamer.so",
+           f"-L{tlib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    return out
 
 
 def _sources(exts=(".cu", ".cuh", ".h")):
@@ -41,6 +64,7 @@ def build(force: bool = False, verbose: bool = False) -> list:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
     outs.append(lib)
+    outs.append(_build_attention(lib, force, verbose))
     hooks = os.path.join(HERE, "libdreamer_testhooks.so")
     if force or not _newer(hooks, deps):
         cmd = ["nvcc", *ARCH, *FLAGS, "-DDREAMER_TEST_HOOKS",

@@ -1,0 +1,178 @@
+"""What the Python entry points of the attention operators refuse, and the memory they return."""
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _ints(v):
+    import torch
+    return torch.tensor(list(v), dtype=torch.int32, device="cuda")
+
+
+def _args(**kw):
+    import torch
+    z = dict(dtype=torch.bfloat16, device="cuda")
+    a = dict(q=torch.ones((6, 4, 64), **z), k=torch.ones((6, 2, 64), **z), v=torch.ones((6, 2, 64), **z),
+             cu_seqlens=_ints([0, 2, 6]))
+    a.update(kw)
+    return a
+
+
+BAD_PACKED = {
+    "q of the host": lambda t: dict(q=t.ones((6, 4, 64))),
+    "no tensor": lambda t: dict(k=None),
+    "a list": lambda t: dict(cu_seqlens=[0, 2, 6]),
+    "two dimensions": lambda t: dict(q=t.ones((6, 256), dtype=t.bfloat16, device="cuda")),
+    "float16": lambda t: dict(q=t.ones((6, 4, 64), dtype=t.float16, device="cuda")),
+    "types that differ": lambda t: dict(k=t.ones((6, 2, 64), device="cuda")),
+    "rows that differ": lambda t: dict(v=t.ones((5, 2, 64), dtype=t.bfloat16, device="cuda")),
+    "heads that differ": lambda t: dict(v=t.ones((6, 1, 64), dtype=t.bfloat16, device="cuda")),
+    "dims that differ": lambda t: dict(k=t.ones((6, 2, 32), dtype=t.bfloat16, device="cuda")),
+    "heads without a group": lambda t: dict(q=t.ones((6, 3, 64), dtype=t.bfloat16, device="cuda")),
+    "no heads": lambda t: dict(q=t.ones((6, 0, 64), dtype=t.bfloat16, device="cuda")),
+    "heads apart": lambda t: dict(q=t.ones((6, 4, 128), dtype=t.bfloat16, device="cuda")[..., :64]),
+    "heads first": lambda t: dict(q=t.ones((4, 6, 64), dtype=t.bfloat16, device="cuda").transpose(0, 1)),
+    "repeated rows": lambda t: dict(q=t.ones((1, 4, 64), dtype=t.bfloat16, device="cuda").expand(6, 4, 64)),
+    "rows off 16 bytes": lambda t: dict(q=t.ones((6, 4 * 64 + 4), dtype=t.bfloat16, device="cuda")[:, :256].view(6, 4, 64)),
+    "a start off 16 bytes": lambda t: dict(q=t.ones(6 * 256 + 4, dtype=t.bfloat16, device="cuda")[4:].view(6, 4, 64)),
+    "boundaries of 64 bits": lambda t: dict(cu_seqlens=t.tensor([0, 2, 6], device="cuda")),
+    "boundaries of the host": lambda t: dict(cu_seqlens=t.tensor([0, 2, 6], dtype=t.int32)),
+    "boundaries apart": lambda t: dict(cu_seqlens=_ints([0, 0, 2, 0, 6, 0])[::2]),
+    "no boundaries": lambda t: dict(cu_seqlens=_ints([])),
+    "an out of another shape": lambda t: dict(out=t.ones((6, 2, 64), dtype=t.bfloat16, device="cuda")),
+    "an out of another type": lambda t: dict(out=t.ones((6, 4, 64), device="cuda")),
+    "a scale of zero": lambda t: dict(scale=0.0),
+    "a scale of nan": lambda t: dict(scale=float("nan")),
+    "a scale past float32": lambda t: dict(scale=1e39),
+    "a status of 64 bits": lambda t: dict(status=t.zeros(1, dtype=t.int64, device="cuda")),
+    "a status of the host": lambda t: dict(status=t.zeros(1, dtype=t.int32)),
+}
+
+
+@pytest.mark.parametrize("what", BAD_PACKED)
+def test_attn_packed_refuses(cuda, what):
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    with pytest.raises(ValueError):
+        attn_packed(**_args(**BAD_PACKED[what](torch)))
+
+
+def test_other_types_and_unsupported_dims(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    from depth_recurrent_attention_b200.dreamer import ERR_UNSUPPORTED, DreamerError
+    with pytest.raises(TypeError):
+        attn_packed(**_args(scale="1"))
+    with pytest.raises(AttributeError):
+        attn_packed(**_args(stream=5))
+    x = torch.ones((6, 2, 32), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(DreamerError) as e:
+        attn_packed(x, x, x, _ints([0, 6]))
+    assert e.value.code == ERR_UNSUPPORTED
+
+
+def test_the_cache_refuses(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    c = KV4Cache.alloc(2, 2, 64, 128, depth=3)
+    assert (c.depth, c.batch, c.n_kv_heads, c.capacity) == (3, 2, 2, 128)
+    z = dict(dtype=torch.bfloat16, device="cuda")
+    k, q, cu, start, lens = torch.ones((5, 2, 64), **z), torch.ones((2, 4, 64), **z), _ints([0, 2, 5]), _ints([0, 0]), _ints([2, 3])
+
+    def refused(fn, *a, error=ValueError, **kw):
+        with pytest.raises(error):
+            fn(*a, **kw)
+
+    refused(KV4Cache, c.data, 128)
+    refused(KV4Cache, c.data, 32)
+    refused(KV4Cache, c.data[..., :-1], 64)
+    refused(KV4Cache, c.data[0], 64)
+    refused(KV4Cache, c.data.view(torch.int8), 64)
+    refused(KV4Cache, c.data.transpose(1, 2), 64)
+    refused(KV4Cache, c.data[:0], 64)
+    refused(KV4Cache, None, 64)
+    for depth in (-1, 3):
+        refused(c.store, k, k, cu, start, depth=depth)
+        refused(c.load, cu, start, 5, depth=depth)
+        refused(c.attend, q, lens, depth=depth)
+    refused(c.store, k, k.float(), cu, start)
+    refused(c.store, k, k[:4], cu, start)
+    refused(c.store, k[:, :1], k[:, :1], cu, start)
+    refused(c.store, k, k, cu[:2], start)
+    refused(c.store, k, k, cu, cu)
+    refused(c.store, k, k, cu.long(), start)
+    refused(c.load, cu, start, -1)
+    refused(c.load, cu, start, 5, dtype=torch.float16)
+    refused(c.load, cu, start, 5, out=(k, k[:4]))
+    refused(c.load, cu, start, 5, dtype=torch.float32, out=(k, k))
+    refused(c.load, cu, start, 1.5, error=TypeError)
+    refused(c.attend, q[:1], lens)
+    refused(c.attend, q[:, :3].contiguous(), lens)
+    refused(c.attend, q, cu)
+    refused(c.attend, q, lens, out=q[:, :2])
+    refused(c.attend, q, lens, scale=float("inf"))
+    refused(c.attend, q, lens, status=torch.zeros(1, device="cuda"))
+    assert not c.data.any()                      # nothing was written
+
+
+def test_no_rows(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache, attn_packed
+    e = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    assert attn_packed(e, e, e, _ints([0])).shape == (0, 2, 64)
+    assert attn_packed(e, e, e, _ints([0, 0])).shape == (0, 2, 64)
+    c = KV4Cache.alloc(1, 2, 64, 64)
+    c.store(e, e, _ints([0, 0]), _ints([0]))
+    k, v = c.load(_ints([0, 0]), _ints([0]), 0)
+    assert k.shape == v.shape == (0, 2, 64) and not c.data.any()
+
+
+def test_one_row_of_any_stride(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    x = torch.randn((1, 2, 64), device="cuda").bfloat16()
+    odd = torch.as_strided(x, (1, 2, 64), (7, 64, 1))
+    assert torch.equal(attn_packed(odd, odd, odd, _ints([0, 1])), x)   # one key: its value
+
+
+def test_out_is_returned_itself_and_references_are_kept_even(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache, attn_packed
+    a = _args(out=torch.zeros((6, 4, 64), dtype=torch.bfloat16, device="cuda"))
+    c = KV4Cache.alloc(1, 2, 64, 64)
+    one, zero = _ints([0, 6]), _ints([0])
+    pair = (torch.empty_like(a["k"]), torch.empty_like(a["v"]))
+    q, lens, o = a["q"][:1].clone(), _ints([6]), torch.empty_like(a["q"][:1])
+    held = [*a.values(), one, zero, pair[0], pair[1], q, lens, o, c.data]
+    refs = [sys.getrefcount(x) for x in held]
+    for _ in range(10):
+        assert attn_packed(**a) is a["out"]
+        c.store(a["k"], a["v"], one, zero)
+        k, v = c.load(one, zero, 6, out=pair)
+        assert k is pair[0] and v is pair[1]
+        assert c.attend(q, lens, out=o) is o
+        with pytest.raises(ValueError):
+            attn_packed(**dict(a, scale=-1.0))
+    del k, v
+    assert [sys.getrefcount(x) for x in held] == refs
+
+
+def test_new_memory_belongs_to_the_stream_of_the_call(cuda):
+    """Blocks that a call allocates on a side stream go back to that stream's pool: the same call
+    again reuses them, and the default stream's allocations never do."""
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    a, s = _args(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = attn_packed(**a, stream=s)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    p = out.data_ptr()
+    del out
+    others = [torch.empty((6, 4, 64), dtype=torch.bfloat16, device="cuda") for _ in range(64)]
+    assert p not in [t.data_ptr() for t in others]
+    with torch.cuda.stream(s):
+        again = [torch.empty((6, 4, 64), dtype=torch.bfloat16, device="cuda") for _ in range(64)]
+    assert p in [t.data_ptr() for t in again]
+    s.synchronize()
