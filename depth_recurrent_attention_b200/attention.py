@@ -1,11 +1,11 @@
-"""Attention operators without a handle: causal attention over packed prompts, and a 4-bit cache of keys and values (quantised as it is
-written, read back, attended by single tokens).
+"""Attention operators without a handle: causal attention over packed prompts, and a 4-bit cache of
+keys and values (quantised as it is written, read back, attended by single tokens).
 
 Every operator runs in libdreamer's CUDA kernels (include/dreamer.h); csrc/attention_py.cpp checks
-arguments and passes pointers (in Python a small call's checks took longer than its kernel).  Tensors are CUDA tensors of one device, float32 or bfloat16;
-rows may be strided (a slice of a fused projection), a row's heads lie densely.  Calls are
-asynchronous on `stream` (default: the current stream of the tensors' device), and forward only:
-outputs carry no gradient.
+arguments and passes pointers (in Python a small call's checks took longer than its kernel).
+Tensors are CUDA tensors of one device, float32 or bfloat16; rows may be strided (a slice of a
+fused projection), a row's heads lie densely.  Calls are asynchronous on `stream` (default: the
+current stream of the tensors' device) and forward only: outputs carry no gradient.
 """
 from __future__ import annotations
 
@@ -17,13 +17,11 @@ from .dreamer import KV4CacheC, _check, lib  # noqa: F401
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 BLOCK = 64  # tokens of a cache block
-GROUP = 64  # channels that share a scale and an offset
-
-
 _fns = None
 
 
 def _lib():
+    """The C entry points with their types (KV4CacheC is dreamer_kv4_cache)."""
     global _fns
     if _fns is None:
         L = lib()
@@ -85,7 +83,8 @@ class KV4Cache:
 
     @staticmethod
     def block_bytes(head_dim: int) -> int:
-        return head_dim // GROUP * BLOCK * 2 * (32 + 4)
+        """Bytes of 64 tokens of one head (0 for a head_dim that has no cache)."""
+        return _lib().dreamer_kv4_bytes(1, 1, head_dim, BLOCK)
 
     @classmethod
     def alloc(cls, batch: int, n_kv_heads: int, head_dim: int, capacity: int, depth: int = 1,
