@@ -103,8 +103,11 @@ __device__ __forceinline__ void check_cu(const PackedArgs &a) {
 }
 
 // ---- bfloat16: tcgen05 ---------------------------------------------------------------------
-// A CTA takes one head and two adjacent 128-query tiles A, B of a prompt that share every K/V block;
-// warp 0 loads Q and K by TMA, warp 2 V, warp 1 issues the MMAs, warps 3-10 hold one query row a thread.
+// An SM holds two 128-query tiles: at head dim 128 one CTA takes two adjacent tiles A, B of a prompt and
+// a head that share every K/V block; at 64 there are two CTAs of one tile (A) each, and while one starts
+// or ends its item the other computes (8 ragged prompts of up to 2048 tokens, 16 heads: 66.4 -> 63.2 us;
+// one prompt of 8192: 244 -> 242).  Warp 0 loads Q and K by TMA, warp 2 V, warp 1 issues the MMAs, warps
+// 4 and up hold one query row a thread.
 // Scores, weights and outputs stay in tensor memory; the output is rescaled only when a row's maximum
 // grows by more than 2^8.  Weights enter the output product as bf16 (half a step of 2^-8 relative each, as
 // the stored output is), their sum is of the float32 values.
@@ -113,6 +116,8 @@ __device__ __forceinline__ void check_cu(const PackedArgs &a) {
 // dim 128 the products take 1020 and the row's part (scores out, maximum, exponentials, weights in) 1750,
 // one after the other for a tile, which two tiles overlap in part; at head dim 64 the products take
 // 960 and the row's parts of both tiles together 2900, of which the exponentials' unit is busy 2048.
+// An item costs 8000 to 10000 cycles beside its blocks (its place in the batch found, first loads and
+// scores, last product and output), which is what short prompts are bound by.
 // So
 //   - head dim 64 keeps the weights in tensor-memory columns of their own, and the next block's
 //     scores are computed as soon as this block's are in registers (one sequence of 8192 tokens, 16
@@ -125,15 +130,19 @@ template <int D>
 struct PkCfg {
   static constexpr int CH = D / 64;                 // 64-column chunks of a head
   static constexpr int TILE = 128 * 128;            // bytes of one [128 x 64] bf16 chunk
-  static constexpr int KST = D == 64 ? 4 : 2;       // K ring depth
-  static constexpr int VST = D == 64 ? 4 : 2;       // V ring depth
-  static constexpr int Q_BYTES = 2 * CH * TILE;     // both query tiles
+  static constexpr int TILES = D == 64 ? 1 : 2;     // query tiles of a CTA
+  static constexpr int CTAS = D == 64 ? 2 : 1;      // CTAs of an SM
+  static constexpr int THREADS = 128 + 128 * TILES;
+  static constexpr int COLS = 512 / CTAS;           // tensor-memory columns
+  static constexpr int KST = D == 64 ? 3 : 2;       // K ring depth
+  static constexpr int VST = 2;                     // V ring depth
+  static constexpr int Q_BYTES = TILES * CH * TILE;
   static constexpr int KV_BYTES = CH * TILE;        // one K (or V) block
   static constexpr int SMEM = Q_BYTES + (KST + VST) * KV_BYTES + 1024 + 256;
   static constexpr bool SEP = D == 64;              // weights in columns of their own
-  static constexpr int P0 = SEP ? 256 : 0, P_STEP = SEP ? 64 : 128;   // weights of tile t: P0 + t * P_STEP
-  static constexpr int O0 = SEP ? 384 : 256;                          // output of tile t: O0 + t * D
-  static_assert(SMEM <= 227 * 1024, "smem");
+  // columns of tile t: scores t * 128, weights P0 + t * 128, output O0 + t * D
+  static constexpr int P0 = SEP ? 128 : 0, O0 = SEP ? 192 : 256;
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "smem");
 };
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -164,13 +173,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
 }
 
 template <int D>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
     packed_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, PackedArgs a) {
   using namespace tc;
   using C = PkCfg<D>;
   constexpr int CH = C::CH, KST = C::KST, VST = C::VST;
   constexpr bool SEP = C::SEP;
+  constexpr int TILES = C::TILES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = smem;
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(352, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % a.Hq;
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(tmem_slot), C::COLS);
     tmem_relinquish();
   }
   if (threadIdx.x == 64) {
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(352, 1)
   pdl_wait();  // inputs of the previous kernel are visible from here on
   if (warp == 0) {
     if (blockIdx.x == 0) check_cu(a);
-    const int3 it = find_item<256>(a, blockIdx.x / a.Hq);
+    const int3 it = find_item<128 * TILES>(a, blockIdx.x / a.Hq);
     if (lane == 0) {
       item_slot[0] = it.x;
       item_slot[1] = it.y;
@@ -233,143 +243,147 @@ __global__ void __launch_bounds__(352, 1)
   const uint32_t tmem = *tmem_slot;
   const int row0 = item_slot[0], S = item_slot[1], pair = item_slot[2];
   if (pair < 0) {  // fewer items than launched
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, C::COLS);
     return;
   }
-  const int qtA = 2 * pair, qtB = 2 * pair + 1;
-  const bool hasB = qtB * 128 < S;
+  const int qtA = TILES * pair, qtB = qtA + 1;
+  const bool hasB = TILES == 2 && qtB * 128 < S;
   const int nbA = qtA + 1, nbB = hasB ? qtB + 1 : 0;
   const int nb = hasB ? nbB : nbA;
-  // TMEM columns: S_A 0..127, S_B 128..255, then see PkCfg
   const uint32_t tS = tmem, tP = tmem + C::P0, tO = tmem + C::O0;
 
-  if (warp == 0 || warp == 2) {
-    // ------------------------------------------------- producers (warp 0: Q, K; warp 2: V)
-    if (lane == 0) {
-      const bool isK = warp == 0;
-      const int colb = (head / a.G) * D;
-      if (isK) {
-        mbar_expect_tx(smem_u32(q_full), (hasB ? 2 : 1) * CH * C::TILE);
-        for (int t = 0; t < (hasB ? 2 : 1); t++)
+  // Registers as the warps need them, of the launch's 256 x 128: 128 x 56 and 128 x 200
+  if (warp < 4) {
+    if (TILES == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 || warp == 2) {
+      // ------------------------------------------------- producers (warp 0: Q, K; warp 2: V)
+      if (lane == 0) {
+        const bool isK = warp == 0;
+        const int colb = (head / a.G) * D;
+        if (isK) {
+          mbar_expect_tx(smem_u32(q_full), (hasB ? 2 : 1) * CH * C::TILE);
+          for (int t = 0; t < (hasB ? 2 : 1); t++)
+            for (int c = 0; c < CH; c++)
+              tma_load_2d(smem_u32(sQ + (t * CH + c) * C::TILE), &tmq, smem_u32(q_full), head * D + 64 * c,
+                          row0 + (t == 0 ? qtA : qtB) * 128);
+        }
+        const CUtensorMap *tm = isK ? &tmk : &tmv;
+        const int NS = isK ? KST : VST;
+        uint64_t *fullb = isK ? k_full : v_full, *emptyb = isK ? k_empty : v_empty;
+        uint8_t *ring = isK ? sK : sV;
+        int issued_ph[4] = {-1, -1, -1, -1};
+        bool ok = true;
+        for (int j = 0; j < nb; j++) {
+          const int s = j % NS;
+          const uint32_t ph = (j / NS) & 1;
+          if (!mbar_wait(smem_u32(&emptyb[s]), ph ^ 1, abort_flag, a.err)) { ok = false; break; }
+          mbar_expect_tx(smem_u32(&fullb[s]), C::KV_BYTES);
           for (int c = 0; c < CH; c++)
-            tma_load_2d(smem_u32(sQ + (t * CH + c) * C::TILE), &tmq, smem_u32(q_full), head * D + 64 * c,
-                        row0 + (t == 0 ? qtA : qtB) * 128);
-      }
-      const CUtensorMap *tm = isK ? &tmk : &tmv;
-      const int NS = isK ? KST : VST;
-      uint64_t *fullb = isK ? k_full : v_full, *emptyb = isK ? k_empty : v_empty;
-      uint8_t *ring = isK ? sK : sV;
-      int issued_ph[4] = {-1, -1, -1, -1};
-      bool ok = true;
-      for (int j = 0; j < nb; j++) {
-        const int s = j % NS;
-        const uint32_t ph = (j / NS) & 1;
-        if (!mbar_wait(smem_u32(&emptyb[s]), ph ^ 1, abort_flag, a.err)) { ok = false; break; }
-        mbar_expect_tx(smem_u32(&fullb[s]), C::KV_BYTES);
-        for (int c = 0; c < CH; c++)
-          tma_load_2d(smem_u32(ring + s * C::KV_BYTES + c * C::TILE), tm, smem_u32(&fullb[s]),
-                      colb + 64 * c, row0 + j * 128);
-        issued_ph[s] = (int)ph;
-      }
-      // every copy issued lands before the CTA can exit
-      const uint64_t t0 = globaltimer();
-      if (isK)
-        while (!mbar_try_wait(smem_u32(q_full), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+            tma_load_2d(smem_u32(ring + s * C::KV_BYTES + c * C::TILE), tm, smem_u32(&fullb[s]),
+                        colb + 64 * c, row0 + j * 128);
+          issued_ph[s] = (int)ph;
         }
-      if (!ok)
-        for (int i = 0; i < NS; i++)
-          if (issued_ph[i] >= 0) {
-            const uint64_t t1 = globaltimer();
-            while (!mbar_try_wait(smem_u32(&fullb[i]), (uint32_t)issued_ph[i]) &&
-                   globaltimer() - t1 < WAIT_LIMIT_NS) {
+        // every copy issued lands before the CTA can exit
+        const uint64_t t0 = globaltimer();
+        if (isK)
+          while (!mbar_try_wait(smem_u32(q_full), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+          }
+        if (!ok)
+          for (int i = 0; i < NS; i++)
+            if (issued_ph[i] >= 0) {
+              const uint64_t t1 = globaltimer();
+              while (!mbar_try_wait(smem_u32(&fullb[i]), (uint32_t)issued_ph[i]) &&
+                     globaltimer() - t1 < WAIT_LIMIT_NS) {
+              }
             }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------- MMA issuer
+      // Per tile S(0); then for each block j (SEP) S(j+1) once S(j) is in registers and P(j) V_j once the
+      // weights are ready, or P(j) V_j and then S(j+1) over them.  The whole warp walks the loop with
+      // values that are the same in every lane and one elected lane issues: a chain of descriptors
+      // computed by one thread of a split warp took longer than the products.
+      constexpr uint32_t ID_S = idesc_bf16_m128(128);
+      constexpr uint32_t ID_PV = idesc_bf16_m128_bmn(D);
+      constexpr uint32_t DESC_HI = (1024 >> 4) | 1u << 14 | 2u << 29;  // 8-row groups 1024 bytes apart, SW128
+      const int uA = __shfl_sync(0xffffffffu, nbA, 0), uB = __shfl_sync(0xffffffffu, nbB, 0);
+      const int un = max(uA, uB);
+      const uint32_t ut = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_lo = smem_u32(sQ) >> 4 | 1u << 16, k_lo = smem_u32(sK) >> 4 | 1u << 16;
+      const uint32_t v_lo = smem_u32(sV) >> 4 | (uint32_t)(C::TILE >> 4) << 16;
+      const bool one = elect_one();
+      auto wait = [&](uint64_t *bar, int n) {
+        const bool r = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), n & 1, abort_flag, a.err));
+        tc_fence_after();
+        return r;
+      };
+      auto commit = [&](uint64_t *bar) {
+        if (one) mma_commit(smem_u32(bar));
+      };
+      auto issue_s = [&](int t, int ks) {
+        if (one) {
+#pragma unroll
+          for (int k = 0; k < D / 16; k++) {
+            const uint32_t off = ((k >> 2) * C::TILE + (k & 3) * 32) >> 4;
+            mma_ss(ut + t * 128, q_lo + ((t * CH * C::TILE) >> 4) + off, k_lo + ks * (C::KV_BYTES >> 4) + off, DESC_HI, ID_S, k != 0);
           }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------- MMA issuer
-    // Per tile S(0); then for each block j (SEP) S(j+1) once S(j) is in registers and P(j) V_j once the
-    // weights are ready, or P(j) V_j and then S(j+1) over them.  The whole warp walks the loop with
-    // values that are the same in every lane and one elected lane issues: a chain of descriptors
-    // computed by one thread of a split warp took longer than the products.
-    constexpr uint32_t ID_S = idesc_bf16_m128(128);
-    constexpr uint32_t ID_PV = idesc_bf16_m128_bmn(D);
-    constexpr uint32_t DESC_HI = (1024 >> 4) | 1u << 14 | 2u << 29;  // 8-row groups 1024 bytes apart, SW128
-    const int uA = __shfl_sync(0xffffffffu, nbA, 0), uB = __shfl_sync(0xffffffffu, nbB, 0);
-    const int un = max(uA, uB);
-    const uint32_t ut = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t q_lo = smem_u32(sQ) >> 4 | 1u << 16, k_lo = smem_u32(sK) >> 4 | 1u << 16;
-    const uint32_t v_lo = smem_u32(sV) >> 4 | (uint32_t)(C::TILE >> 4) << 16;
-    const bool one = elect_one();
-    auto wait = [&](uint64_t *bar, int n) {
-      const bool r = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), n & 1, abort_flag, a.err));
-      tc_fence_after();
-      return r;
-    };
-    auto commit = [&](uint64_t *bar) {
-      if (one) mma_commit(smem_u32(bar));
-    };
-    auto issue_s = [&](int t, int ks) {
-      if (one) {
-#pragma unroll
-        for (int k = 0; k < D / 16; k++) {
-          const uint32_t off = ((k >> 2) * C::TILE + (k & 3) * 32) >> 4;
-          mma_ss(ut + t * 128, q_lo + ((t * CH * C::TILE) >> 4) + off, k_lo + ks * (C::KV_BYTES >> 4) + off, DESC_HI, ID_S, k != 0);
         }
-      }
-    };
-    auto issue_pv = [&](int t, int j, int vs) {  // 128 keys, 16 per instruction (8 TMEM columns of P)
-      if (j + 1 == (t == 0 ? uA : uB) && by_rows[t]) return;
-      if (one) {
+      };
+      auto issue_pv = [&](int t, int j, int vs) {  // 128 keys, 16 per instruction (8 TMEM columns of P)
+        if (j + 1 == (t == 0 ? uA : uB) && by_rows[t]) return;
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < 8; k++)
-          mma_ts(ut + C::O0 + t * D, ut + C::P0 + t * C::P_STEP + k * 8, v_lo + vs * (C::KV_BYTES >> 4) + k * 128, DESC_HI,
-                 ID_PV, k == 0 ? (uint32_t)j : 1u);
+          for (int k = 0; k < 8; k++)
+            mma_ts(ut + C::O0 + t * D, ut + C::P0 + t * 128 + k * 8, v_lo + vs * (C::KV_BYTES >> 4) + k * 128, DESC_HI,
+                   ID_PV, k == 0 ? (uint32_t)j : 1u);
+        }
+      };
+      bool ok = wait(q_full, 0) && wait(&k_full[0], 0);
+      if (ok) {
+        issue_s(0, 0);
+        commit(&s_full[0]);
+        if (uB > 0) {
+          issue_s(1, 0);
+          commit(&s_full[1]);
+        }
+        commit(&k_empty[0]);
       }
-    };
-    bool ok = wait(q_full, 0) && wait(&k_full[0], 0);
-    if (ok) {
-      issue_s(0, 0);
-      commit(&s_full[0]);
-      if (uB > 0) {
-        issue_s(1, 0);
-        commit(&s_full[1]);
-      }
-      commit(&k_empty[0]);
-    }
-    int vs = 0, ks = 1 % KST;  // stages of block j's values and of block j + 1's keys
-    for (int j = 0; j < un && ok; j++) {
-      const bool next = j + 1 < un;
-      if (SEP && next) {
-        if (!wait(&k_full[ks], (j + 1) / KST)) break;
+      int vs = 0, ks = 1 % KST;  // stages of block j's values and of block j + 1's keys
+      for (int j = 0; j < un && ok; j++) {
+        const bool next = j + 1 < un;
+        if (SEP && next) {
+          if (!wait(&k_full[ks], (j + 1) / KST)) break;
 #pragma unroll
-        for (int t = 0; t < 2; t++)
-          if (ok && j + 1 < (t == 0 ? uA : uB)) {
-            ok = wait(&s_read[t], j);
-            if (ok) issue_s(t, ks);
-            if (ok) commit(&s_full[t]);
+          for (int t = 0; t < TILES; t++)
+            if (ok && j + 1 < (t == 0 ? uA : uB)) {
+              ok = wait(&s_read[t], j);
+              if (ok) issue_s(t, ks);
+              if (ok) commit(&s_full[t]);
+            }
+          if (ok) commit(&k_empty[ks]);
+        }
+        if (!ok || !wait(&v_full[vs], j / VST)) break;
+        if (!SEP && next && !wait(&k_full[ks], (j + 1) / KST)) break;
+#pragma unroll
+        for (int t = 0; t < TILES; t++)
+          if (ok && j < (t == 0 ? uA : uB)) {
+            ok = wait(&p_full[t], j);
+            if (!ok) break;
+            issue_pv(t, j, vs);
+            if (!SEP && j + 1 < (t == 0 ? uA : uB)) issue_s(t, ks);
+            commit(SEP ? &pv_done[t] : &s_full[t]);
           }
-        if (ok) commit(&k_empty[ks]);
+        if (!ok) break;
+        commit(&v_empty[vs]);
+        if (!SEP && next) commit(&k_empty[ks]);
+        if (++vs == VST) vs = 0;
+        if (++ks == KST) ks = 0;
       }
-      if (!ok || !wait(&v_full[vs], j / VST)) break;
-      if (!SEP && next && !wait(&k_full[ks], (j + 1) / KST)) break;
-#pragma unroll
-      for (int t = 0; t < 2; t++)
-        if (ok && j < (t == 0 ? uA : uB)) {
-          ok = wait(&p_full[t], j);
-          if (!ok) break;
-          issue_pv(t, j, vs);
-          if (!SEP && j + 1 < (t == 0 ? uA : uB)) issue_s(t, ks);
-          commit(SEP ? &pv_done[t] : &s_full[t]);
-        }
-      if (!ok) break;
-      commit(&v_empty[vs]);
-      if (!SEP && next) commit(&k_empty[ks]);
-      if (++vs == VST) vs = 0;
-      if (++ks == KST) ks = 0;
     }
-  } else if (warp >= 3) {
-    // ------------------------------------------------- softmax (tile A: warps 3-6, B: 7-10)
-    const int t = warp < 7 ? 0 : 1;
+  } else {
+    if (TILES == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ------------------------------------------------- softmax (tile A: warps 4-7, B: 8-11)
+    const int t = warp < 8 ? 0 : 1;
     const int nbt = t == 0 ? nbA : nbB;
     const int qt = t == 0 ? qtA : qtB;
     if (nbt > 0) {
@@ -378,7 +392,7 @@ __global__ void __launch_bounds__(352, 1)
       const int qi = qt * 128 + row;               // query position in the prompt
       const uint32_t lane_off = (uint32_t)(q * 32) << 16;
       const uint32_t sbuf = tS + t * 128 + lane_off;
-      const uint32_t pbuf = tP + t * C::P_STEP + lane_off;
+      const uint32_t pbuf = tP + t * 128 + lane_off;
       const uint32_t obuf = tO + t * D + lane_off;
       // the same answer in every lane: what follows is done by whole warps
       auto wait_warp = [&](uint64_t *bar, int n) {
@@ -555,7 +569,7 @@ __global__ void __launch_bounds__(352, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::COLS);
   }
 }
 
@@ -802,6 +816,13 @@ long most_tiles(long n_tokens, long n_seq, long rows) {
   return (n_tokens + full * (rows - 1)) / rows;
 }
 
+template <int D, typename... A>
+int launch_tc(const PackedAttn &p, cudaStream_t s, LaunchOpt o, const A &...args) {
+  using C = PkCfg<D>;
+  return launch_items<packed_tc_kernel<D>>(most_tiles(p.n_tokens, p.n_seq, 128 * C::TILES) * p.Hq, C::THREADS, C::SMEM, s, o,
+                                           args...);
+}
+
 }  // namespace
 
 int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
@@ -818,9 +839,8 @@ int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
         !row_map(&tk, p.k, (uint64_t)p.Hkv * p.d, p.n_tokens, p.ldk) ||
         !row_map(&tv, p.v, (uint64_t)p.Hkv * p.d, p.n_tokens, p.ldv))
       return DREAMER_ERR_CUDA;
-    const long items = most_tiles(p.n_tokens, p.n_seq, 256) * p.Hq;
-    if (p.d == 64) return launch_items<packed_tc_kernel<64>>(items, 352, PkCfg<64>::SMEM, s, o, tq, tk, tv, a);
-    return launch_items<packed_tc_kernel<128>>(items, 352, PkCfg<128>::SMEM, s, o, tq, tk, tv, a);
+    if (p.d == 64) return launch_tc<64>(p, s, o, tq, tk, tv, a);
+    return launch_tc<128>(p, s, o, tq, tk, tv, a);
   }
   const long items = most_tiles(p.n_tokens, p.n_seq, 32) * p.Hq;
   switch (p.d) {
