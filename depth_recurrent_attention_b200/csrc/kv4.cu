@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
 // The rows r of a 16-key tile are the keys perm_row(r): with it a warp's 8-byte reads of K rows and
 // 4-byte reads of V rows meet every bank once.
 //
-// Measured: the decode workload's depth (64 sequences of 4096 tokens, 16 heads of 64, 302 MB) 56 us, 5.4
+// Measured: the decode workload's depth (64 sequences of 4096 tokens, 16 heads of 64, 302 MB) 53 us, 5.7
 // TB/s, with the cluster form at one CTA an item; products on bf16 numbers instead of bytes took 82.
 struct AttnArgs {
   const uint8_t *data;
@@ -468,10 +468,10 @@ struct WarpAttn {
       if constexpr (INT) {
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 127 * 256 steps to the largest |q|; a q that is not finite leaves sum(q) so, and its
-        // scores with it.  The step is kept a normal number (values that small add nothing).
-        const bool ok = amax >= 0x1p-110f && amax <= 0x1.fffffep127f;
-        const float step = ok ? amax / 32512.f : 1.f, inv = ok ? 32512.f / amax : 0.f;
+        // 127 * 256 steps to the largest |q|, or to 2^-110 (the step stays a normal number); a q that is
+        // not finite leaves sum(q) so, and its scores with it
+        const bool ok = amax <= 0x1.fffffep127f;
+        const float top = ok ? fmaxf(amax, 0x1p-110f) : 1.f, step = top / 32512.f, inv = 32512.f / top;
         qi[p][0] = __shfl_sync(0xffffffffu, step, c0) * scale_log2;
         qi[p][1] = __shfl_sync(0xffffffffu, step, c1) * scale_log2;
 #pragma unroll
@@ -701,8 +701,9 @@ struct WarpAttn {
       t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, k));
       t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, k));
     }
-    const float i0 = t0 >= 0x1p-110f ? __fdividef(65535.f, t0) : 0.f;
-    const float i1 = t1 >= 0x1p-110f ? __fdividef(65535.f, t1) : 0.f;
+    t0 = fmaxf(t0, 0x1p-110f);  // the step stays a normal number
+    t1 = fmaxf(t1, 0x1p-110f);
+    const float i0 = __fdividef(65535.f, t0), i1 = __fdividef(65535.f, t1);
     uint32_t hb[4], lb[4];
     uint32_t lo[NSUP], hi[NSUP];  // bytes of column g's weights of the tile's rows 2t, 2t + 1, 8 + 2t, 8 + 2t + 1
 #pragma unroll

@@ -197,6 +197,19 @@ class Dreamer:
                                          _stream(stream)), "dreamer_decode_step")
         return x_out
 
+    def _states(self, name, t, rows=None):
+        """Tokens' states [rows][hidden] of the handle's type, contiguous on a GPU."""
+        want = torch.float32 if self.cfg.dtype == "fp32" else torch.bfloat16
+        if not t.is_cuda or t.dtype is not want or t.dim() != 2 or t.shape[1] != self.cfg.hidden or \
+                not t.is_contiguous() or (rows is not None and t.shape[0] != rows):
+            raise ValueError(f"{name}: a contiguous CUDA tensor [{rows or 'tokens'}][{self.cfg.hidden}] of {want}")
+
+    @staticmethod
+    def _counts(name, t, n=None):
+        if not t.is_cuda or t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
+                (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name}: a contiguous CUDA int32 tensor [{n or 'prompts + 1'}]")
+
     def forward_packed(self, x_in, cu_seqlens, x_out=None, depth_begin=0, depth_end=None,
                        da_kv=None, trace: dict | None = None, stream=None):
         """The forward over packed prompts of any lengths: x_in [tokens][hidden], cu_seqlens a CUDA
@@ -204,11 +217,11 @@ class Dreamer:
         the rows that KV4Cache.store takes."""
         cfg = self.cfg
         depth_end = cfg.depth if depth_end is None else depth_end
-        if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or cu_seqlens.dim() != 1 or \
-                not cu_seqlens.is_contiguous():
-            raise ValueError("cu_seqlens: a contiguous CUDA int32 tensor [prompts + 1]")
+        self._states("x_in", x_in)
+        self._counts("cu_seqlens", cu_seqlens)
         if x_out is None:
             x_out = torch.empty_like(x_in)
+        self._states("x_out", x_out, x_in.shape[0])
         tr = self._trace(trace)
         _check(self.L.dreamer_core_forward_packed(
             self.h, _ptr(x_in), _ptr(x_out), _ptr(cu_seqlens), int(cu_seqlens.shape[0]) - 1,
@@ -223,8 +236,11 @@ class Dreamer:
         quantised into position cache_len[b] of every depth, and cache_len[b] + 1 are attended."""
         if cache.depth != self.cfg.depth:
             raise ValueError(f"cache: {self.cfg.depth} depths, not {cache.depth}")
+        self._states("x_new", x_new, self.cfg.batch)
+        self._counts("cache_len", cache_len, self.cfg.batch)
         if x_out is None:
             x_out = torch.empty_like(x_new)
+        self._states("x_out", x_out, self.cfg.batch)
         tr = self._trace(trace)
         cc = KV4CacheC(cache.data.data_ptr(), cache.batch, cache.n_kv_heads, cache.head_dim,
                        cache.capacity)

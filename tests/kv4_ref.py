@@ -61,7 +61,7 @@ def unpack(data, d):
     return np.stack(codes), np.stack(s), np.stack(m)
 
 
-def attend(data, d, q, lens, scale, out_eps):
+def attend(data, d, q, lens, scale, out_eps, floor=2.0 ** -102):
     """(output, tolerance) [B][Hq][d] of one query token a sequence.
 
     The tolerance counts, per element, with unit roundoffs u = 2^-23 (float32, either rounding
@@ -76,7 +76,9 @@ def attend(data, d, q, lens, scale, out_eps):
     bfloat16 (out_eps 2^-8) scores are taken with q in steps of its plane's largest |q| / 32512: each
     q is off by half a step at most, so E has scale sum over planes of (half a step) sum s c more.
     Its weights w_j s_j are taken in steps of the largest of a block of 64 keys / 65535: sum over
-    blocks of half a step times sum c.
+    blocks of half a step times sum c.  Neither step is below that of a largest of 2^-110; weights are
+    relative to a maximum that is at most 2^8 behind, so w_j s_j count from `floor` = 2^-102 on, and from
+    2^-110 on where there is one block.
     """
     codes, s, m = unpack(data, d)
     B, Hq, _ = q.shape
@@ -101,7 +103,7 @@ def attend(data, d, q, lens, scale, out_eps):
             aq = np.abs(qq).reshape(-1, 64)
             e = (np.abs(kc - 8) * ks[..., None] * aq).sum((1, 2)) + (np.abs(km + 8 * ks) * aq.sum(-1)).sum(1)
             if out_eps == 2.0 ** -8:
-                e = e + (aq.max(-1) / 65024 * (kc * ks[..., None]).sum(-1)).sum(-1) / ((d + 8) * u)
+                e = e + (np.maximum(aq.max(-1), 2.0 ** -110) / 65024 * (kc * ks[..., None]).sum(-1)).sum(-1) / ((d + 8) * u)
             E = (d + 8) * u * abs(scale) * e.max() + 2.0 ** -21 + u * (1 + np.abs(z - z.max()).max())
             absv = w @ np.abs(v) + w @ (np.abs(vm + 8 * vs)[..., None] + np.zeros((1, 1, 64))).reshape(n, d)
             spread = w @ (np.abs(vc - 8) * vs[..., None]).reshape(n, d)
@@ -109,7 +111,7 @@ def attend(data, d, q, lens, scale, out_eps):
             if out_eps == 2.0 ** -8:
                 spread = np.zeros(d)
                 for j in range(0, n, 64):
-                    step = (w[j:j + 64, None] * vs[j:j + 64]).max(0) / 65535         # [ng]
+                    step = np.maximum((w[j:j + 64, None] * vs[j:j + 64]).max(0), floor) / 65535   # [ng]
                     spread += (step[:, None] / 2 * vc[j:j + 64].sum(0)).reshape(d)
                 tol[b, h] = out_eps * np.abs(o) + spread
             else:

@@ -183,6 +183,24 @@ def test_attend_against_64_bits(cuda, dtype, lens, H, G, d, capacity):
     assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
 
 
+@pytest.mark.parametrize("dtype,small", [("bf16", -110), ("fp32", -100)])
+def test_attend_of_small_numbers(cuda, dtype, small):
+    """Queries and values near the least normal numbers count as others do: queries of 2^-112 over keys
+    of 2^98, values of 2^-110 (float32: 2^-100, whose third bfloat16 term is a normal number)."""
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    rng = np.random.default_rng(21)
+    k, v = rng.standard_normal((2, 40, 2, 64))
+    c = KV4Cache.alloc(1, 2, 64, 64)
+    c.store(_t(k * 2.0 ** 97, dtype), _t(v * 2.0 ** small, dtype), _ints([0, 40]), _ints([0]))
+    q = _t(rng.standard_normal((1, 4, 64)) * 2.0 ** (small - 3), dtype)
+    scale = 2.0 ** (-97 - small)
+    out = c.attend(q, _ints([40]), scale=scale)
+    ref, tol = R.attend(c.data[0].cpu().numpy(), 64, _f64(q), [40], scale, EPS[dtype], floor=2.0 ** -110)
+    err = np.abs(_f64(out) - ref)
+    assert (err <= tol).all(), (err / tol).max()
+    assert (tol.max(-1) < np.abs(ref).max(-1) / 4).all()
+
+
 @pytest.mark.parametrize("capacity", [192, 192 * 70])
 def test_attend_does_not_use_what_lies_behind_the_last_key(cuda, capacity):
     """NaN pairs and random codes behind lens[b] change no bit."""

@@ -304,3 +304,30 @@ def test_refusals(cuda):
     with pytest.raises(ValueError):
         dev.decode_step_kv4(x[:2], KV4Cache.alloc(2, 8, 64, 192, depth=1), _ints([0, 0]))
     dev.close()
+
+
+def test_tensors_that_the_binding_refuses(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    cfg = configs.SMALL.with_(batch=2, seq=64, depth=2, **FREE)
+    dev = _handle(cfg, inputs.host_weights(cfg), max_cache_len=64)
+    x = inputs.to_device(inputs.extra_normal(cfg, 1, (16, cfg.hidden), 1.0), "bf16")
+    cu, c, lens = _ints([0, 8]), KV4Cache.alloc(2, 8, 64, 64, depth=2), _ints([0, 3])
+    for bad in (x[:8].float(), x[:8].cpu(), x[:8, :64], x[::2], x[:8].view(-1), x[:8, :64].contiguous()):
+        for kw in (dict(x_in=bad), dict(x_in=x[:8], x_out=bad)):
+            with pytest.raises(ValueError):
+                dev.forward_packed(cu_seqlens=cu, **kw)
+    with pytest.raises(ValueError):
+        dev.forward_packed(x[:8], cu, x_out=x[:9].clone())
+    for bad in (cu.long(), cu.cpu(), cu.view(1, 2), _ints([0, 0, 8, 8])[::2]):
+        with pytest.raises(ValueError):
+            dev.forward_packed(x[:8], bad)
+    for bad in (x[:1], x[:3], x[:2].float(), x[:2].cpu(), x[:4:2]):
+        for kw in (dict(x_new=bad), dict(x_new=x[:2], x_out=bad)):
+            with pytest.raises(ValueError):
+                dev.decode_step_kv4(cache=c, cache_len=lens, **kw)
+    for bad in (lens.long(), lens.cpu(), lens[:1], _ints([0, 0, 0])):
+        with pytest.raises(ValueError):
+            dev.decode_step_kv4(x[:2], c, bad)
+    assert not c.data.any()
+    dev.close()
