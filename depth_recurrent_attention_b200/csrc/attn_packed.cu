@@ -574,26 +574,36 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
 }
 
 // ---- float32: CUDA cores -------------------------------------------------------------------
-// A CTA takes one head and 32 query rows of a prompt; its two groups of 128 threads take the
-// 64-key blocks in turns, each with its own softmax and buffers (one group's loads run beside the
-// other's arithmetic, and a long row's chain of blocks is half as long), and join at the end.  A
+// A CTA takes one head and 32 query rows of a prompt; its groups of 128 threads take the 64-key
+// blocks in turns, each with its own softmax and buffers (one group's loads run beside the
+// others' arithmetic, and a long row's chain of blocks is cut by their number), and join at the end.  A
 // group's threads form an 8 x 16 grid: 4 rows x 4 keys (tx, tx + 16, ..) of the scores and 4 rows x
 // D / 16 columns of the output each.  Q and K rows are padded by 4 words, so that eight rows' 16-byte
-// reads meet every bank once; a step of 4 channels reads eight words of 16 bytes for 64 multiply-adds.
-template <int D>
+// reads meet every bank once; a step of 4 channels reads eight words of 16 bytes for 64 multiply-adds,
+// issued as 32 of pairs (359 -> 345 us, 8 prompts of up to 2000 tokens, 8 heads of 64: half of the
+// multiply-add rate, bound by issue and shared memory; copies a block ahead measured no faster).
+//
+// Two groups a CTA and two CTAs an SM (one at head dim 128); four groups and one CTA where the items
+// would not keep that many busy, and the chain of the longest row decides (long_chains).
+template <int D, int NG>
 struct F32Cfg {
   static constexpr int BM = 32, BN = 64;
+  static constexpr int GROUPS = NG;  // of 128 threads
+  static constexpr int CTAS = D <= 64 && NG == 2 ? 2 : 1;
+  static constexpr int THREADS = 128 * GROUPS;
   static constexpr int RP = D + 4;   // padded row of Q and K
   static constexpr int PP = BM + 4;  // padded row of the weights [key][row]
   static constexpr int GROUP = BN * RP + BN * D + BN * PP;  // floats of a group's K, V, weights
-  static constexpr int SMEM = (BM * RP + 2 * GROUP) * 4;
+  static constexpr int SMEM = (BM * RP + GROUPS * GROUP) * 4;
 };
 
-template <int D>
-__global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(PackedArgs a) {
-  using C = F32Cfg<D>;
+template <int D, int NG>
+__global__ void __launch_bounds__(F32Cfg<D, NG>::THREADS, F32Cfg<D, NG>::CTAS) packed_f32_kernel(PackedArgs a) {
+  using C = F32Cfg<D, NG>;
   constexpr int BM = C::BM, BN = C::BN, RP = C::RP, PP = C::PP;
   constexpr int OC = D / 16;  // output columns of a thread
+  constexpr int KJ = BN / 16;  // and keys of a block
+  constexpr int GROUPS = C::GROUPS;
   extern __shared__ __align__(16) float fsm[];
   __shared__ int item[3];
   pdl_wait();
@@ -629,7 +639,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
   };
   auto landed = [] { asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory"); };
   auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
-  fetch(a.q, a.ldq, q0, BM, head * D, sQ, RP, threadIdx.x, 256);
+  fetch(a.q, a.ldq, q0, BM, head * D, sQ, RP, threadIdx.x, C::THREADS);
   landed();
   __syncthreads();
   float o[4][OC], m[4], l[4];
@@ -641,32 +651,37 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
     for (int c = 0; c < OC; c++) o[i][c] = 0.f;
   }
   const int last = min(S, q0 + BM);  // keys of the tile's last row
-  for (int k0 = group * BN; k0 < last; k0 += 2 * BN) {
+  for (int k0 = group * BN; k0 < last; k0 += GROUPS * BN) {
     group_sync();  // the block before is done with
     fetch(a.k, a.ldk, k0, BN, kvh * D, sK, RP, tid, 128);
     fetch(a.v, a.ldv, k0, BN, kvh * D, sV, D, tid, 128);
     landed();
     group_sync();
-    float s[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) s[i][j] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      float4 qa[4], ka[4];
-#pragma unroll
-      for (int i = 0; i < 4; i++) qa[i] = *reinterpret_cast<const float4 *>(sQ + (4 * ty + i) * RP + d);
-#pragma unroll
-      for (int j = 0; j < 4; j++) ka[j] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * RP + d);
+    float s[4][KJ];
+    {
+      uint64_t s2[4][KJ];  // sums of even and of odd channels
 #pragma unroll
       for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          s[i][j] = fmaf(qa[i].x, ka[j].x, s[i][j]);
-          s[i][j] = fmaf(qa[i].y, ka[j].y, s[i][j]);
-          s[i][j] = fmaf(qa[i].z, ka[j].z, s[i][j]);
-          s[i][j] = fmaf(qa[i].w, ka[j].w, s[i][j]);
+        for (int j = 0; j < KJ; j++) s2[i][j] = 0ull;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        ulonglong2 qa[4], ka[KJ];
+#pragma unroll
+        for (int i = 0; i < 4; i++) qa[i] = *reinterpret_cast<const ulonglong2 *>(sQ + (4 * ty + i) * RP + d);
+#pragma unroll
+        for (int j = 0; j < KJ; j++) ka[j] = *reinterpret_cast<const ulonglong2 *>(sK + (tx + 16 * j) * RP + d);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int j = 0; j < KJ; j++) s2[i][j] = f2_fma(qa[i].y, ka[j].y, f2_fma(qa[i].x, ka[j].x, s2[i][j]));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < KJ; j++) {
+          const float2 u = f2_unpack(s2[i][j]);
+          s[i][j] = u.x + u.y;
         }
     }
     const bool diag = k0 + BN > q0;  // some key of the block is behind some row
@@ -674,7 +689,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
     for (int i = 0; i < 4; i++) {
       float mx = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
+      for (int j = 0; j < KJ; j++) {
         s[i][j] *= a.scale_log2;
         if (diag && k0 + tx + 16 * j > q0 + 4 * ty + i) s[i][j] = -INFINITY;
         mx = fmaxf(mx, s[i][j]);
@@ -686,7 +701,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
       const float alpha = m[i] == -INFINITY ? 0.f : exp2f(m[i] - base);
       float ps = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
+      for (int j = 0; j < KJ; j++) {
         s[i][j] = exp2f(s[i][j] - base);
         ps += s[i][j];
       }
@@ -699,7 +714,7 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
       m[i] = mn;
     }
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+    for (int j = 0; j < KJ; j++)
       *reinterpret_cast<float4 *>(sP + (tx + 16 * j) * PP + 4 * ty) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
     __syncwarp();  // a row's weights are written and read by the same half warp
     const int nk = min(BN, last - k0);
@@ -721,8 +736,16 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         if (DIAG && k0 + k > q0 + 4 * ty + i) continue;  // 0 x infinity stays out
+        if constexpr (OC >= 2) {
 #pragma unroll
-        for (int c = 0; c < OC; c++) o[i][c] = fmaf(pa[i], va[c], o[i][c]);
+          for (int c = 0; c < OC; c += 2) {
+            const float2 u = f2_unpack(f2_fma(f2_pack(pa[i], pa[i]), f2_pack(va[c], va[c + 1]), f2_pack(o[i][c], o[i][c + 1])));
+            o[i][c] = u.x;
+            o[i][c + 1] = u.y;
+          }
+        } else {
+          o[i][0] = fmaf(pa[i], va[0], o[i][0]);
+        }
       }
     };
     if (!diag) {
@@ -733,10 +756,10 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
       for (int k = 0; k < nk; k++) out_step(k, std::true_type());
     }
   }
-  // the second group's sums over its own buffers, where the first one takes them in
-  float *x = fsm + BM * RP + C::GROUP;  // [4 * OC + 8][128]
+  // the other groups' sums over their own buffers, where the first one takes them in
   static_assert(C::GROUP >= (4 * OC + 8) * 128, "join buffer");
-  if (group == 1) {
+  if (group > 0) {
+    float *x = sK;  // [4 * OC + 8][128]
     group_sync();
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -747,15 +770,20 @@ __global__ void __launch_bounds__(256, D <= 64 ? 2 : 1) packed_f32_kernel(Packed
     }
   }
   __syncthreads();
-  if (group == 1) return;
+  if (group > 0) return;
+  const int groups = min(GROUPS, (last + BN - 1) / BN);  // those with a key
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const float m1 = x[(4 * OC + i) * 128 + tid], mn = fmaxf(m[i], m1);
-    // a group without a key holds zeros
-    const float f0 = m[i] == -INFINITY ? 1.f : exp2f(m[i] - mn), f1 = m1 == -INFINITY ? 1.f : exp2f(m1 - mn);
-    l[i] = fmaf(f1, x[(4 * OC + 4 + i) * 128 + tid], l[i] * f0);
+    for (int gr = 1; gr < groups; gr++) {
+      const float *x = sK + gr * C::GROUP;
+      const float m1 = x[(4 * OC + i) * 128 + tid], mn = fmaxf(m[i], m1);
+      // a group without a visible key holds zeros
+      const float f0 = m[i] == -INFINITY ? 1.f : exp2f(m[i] - mn), f1 = m1 == -INFINITY ? 1.f : exp2f(m1 - mn);
+      l[i] = fmaf(f1, x[(4 * OC + 4 + i) * 128 + tid], l[i] * f0);
 #pragma unroll
-    for (int c = 0; c < OC; c++) o[i][c] = fmaf(f1, x[(i * OC + c) * 128 + tid], o[i][c] * f0);
+      for (int c = 0; c < OC; c++) o[i][c] = fmaf(f1, x[(i * OC + c) * 128 + tid], o[i][c] * f0);
+      m[i] = mn;
+    }
 #pragma unroll
     for (int k = 1; k < 16; k <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], k);
     const int r = q0 + 4 * ty + i;
@@ -823,6 +851,27 @@ int launch_tc(const PackedAttn &p, cudaStream_t s, LaunchOpt o, const A &...args
                                            args...);
 }
 
+// Four groups a CTA where there are at most two and a half items an SM and the prompts are longer than
+// two groups' blocks on average (head dim 64; four against two groups): a prompt of 2000 tokens, 4 heads
+// (252 items) 71 us against 99; four of up to 1000, 4 heads 47 against 59; the same with 16 heads (1100
+// items) 175 against 144; four of up to 128, 16 heads 13 against 11.  At head dim 128 both measured
+// the same.
+bool long_chains(const PackedAttn &p, long items) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return false;
+  return 2 * items <= 5L * sms && p.n_tokens > 128L * p.n_seq;
+}
+
+template <int D>
+int launch_f32(const PackedAttn &p, cudaStream_t s, LaunchOpt o, const PackedArgs &a) {
+  const long items = most_tiles(p.n_tokens, p.n_seq, 32) * p.Hq;
+  if constexpr (D <= 64)
+    if (long_chains(p, items))
+      return launch_items<packed_f32_kernel<D, 4>>(items, F32Cfg<D, 4>::THREADS, F32Cfg<D, 4>::SMEM, s, o, a);
+  return launch_items<packed_f32_kernel<D, 2>>(items, F32Cfg<D, 2>::THREADS, F32Cfg<D, 2>::SMEM, s, o, a);
+}
+
 }  // namespace
 
 int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
@@ -842,12 +891,11 @@ int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
     if (p.d == 64) return launch_tc<64>(p, s, o, tq, tk, tv, a);
     return launch_tc<128>(p, s, o, tq, tk, tv, a);
   }
-  const long items = most_tiles(p.n_tokens, p.n_seq, 32) * p.Hq;
   switch (p.d) {
-    case 16: return launch_items<packed_f32_kernel<16>>(items, 256, F32Cfg<16>::SMEM, s, o, a);
-    case 32: return launch_items<packed_f32_kernel<32>>(items, 256, F32Cfg<32>::SMEM, s, o, a);
-    case 64: return launch_items<packed_f32_kernel<64>>(items, 256, F32Cfg<64>::SMEM, s, o, a);
-    default: return launch_items<packed_f32_kernel<128>>(items, 256, F32Cfg<128>::SMEM, s, o, a);
+    case 16: return launch_f32<16>(p, s, o, a);
+    case 32: return launch_f32<32>(p, s, o, a);
+    case 64: return launch_f32<64>(p, s, o, a);
+    default: return launch_f32<128>(p, s, o, a);
   }
 }
 

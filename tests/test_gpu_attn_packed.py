@@ -101,6 +101,27 @@ def test_packed_against_64_bits(cuda, dtype, d, lens, Hq, Hk):
     _check(_f64(out), want, tol, np.ones(sum(lens), bool))
 
 
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("Hq", [2, 24])       # few items with long rows, and many: two ways to share a row's keys
+def test_float32_of_few_and_of_many_items(cuda, Hq, d):
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    lens = [257, 1, 480]
+    rng = np.random.default_rng(Hq + d)
+    q, k, v = _qkv(rng, sum(lens), Hq, 2, d, "fp32")
+    cu = [0, 257, 258, 738]
+    out = attn_packed(q, k, v, _ints(cu))
+    want, tol = reference(_f64(q), _f64(k), _f64(v), cu, d ** -0.5, "fp32")
+    _check(_f64(out), want, tol, np.ones(sum(lens), bool))
+    assert torch.equal(out, attn_packed(q, k, v, _ints(cu)))
+    for r, bad in ((40, np.inf), (300, np.nan), (257 + 1 + 190, -np.inf)):
+        v[r, 1, 3] = bad
+    want, tol = reference(_f64(q), _f64(k), _f64(v), cu, d ** -0.5, "fp32")
+    got, fin = _f64(attn_packed(q, k, v, _ints(cu))), np.isfinite(want)
+    assert np.array_equal(np.isfinite(got), fin)
+    assert (np.abs(got - want)[fin] <= tol[fin]).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_strides_scale_and_rows_of_no_prompt(cuda, dtype):
     """q, k, v as slices of one fused projection, a given scale, rows before the first and behind
