@@ -922,5 +922,5 @@ extern "C" int dreamer_attn_packed(const void *q, int64_t ldq, const void *k, in
   }
   ops::PackedAttn p{q, ldq, k, ldk, v, ldv, out, ldo, cu_seqlens, n_seq, n_tokens, n_heads, n_kv_heads,
                     head_dim, dtype, scale, nullptr, status};
-  return ops::attn_packed(p, (cudaStream_t)stream);
+  return ops::attn_packed(p, (cudaStream_t)stream, ops::user_launch((cudaStream_t)stream));
 }

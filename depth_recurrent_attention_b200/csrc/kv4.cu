@@ -1532,7 +1532,7 @@ extern "C" int dreamer_kv4_store(const dreamer_kv4_cache *c, const void *k, int6
   const int rc = check_rows(c, k, ldk, v, ldv, cu_rows, start, n_rows, dtype);
   if (rc) return rc;
   return ops::kv4_store(to_cache(c), ops::Kv4Rows{k, v, ldk, ldv, cu_rows, start, n_rows, dtype, 0, status},
-                        (cudaStream_t)stream);
+                        (cudaStream_t)stream, ops::user_launch((cudaStream_t)stream));
 }
 
 extern "C" int dreamer_kv4_load(const dreamer_kv4_cache *c, void *k, int64_t ldk, void *v, int64_t ldv,
@@ -1541,7 +1541,7 @@ extern "C" int dreamer_kv4_load(const dreamer_kv4_cache *c, void *k, int64_t ldk
   const int rc = check_rows(c, k, ldk, v, ldv, cu_rows, start, n_rows, dtype);
   if (rc) return rc;
   return ops::kv4_load(to_cache(c), ops::Kv4Rows{k, v, ldk, ldv, cu_rows, start, n_rows, dtype, zero_rest ? 1 : 0, status},
-                       (cudaStream_t)stream);
+                       (cudaStream_t)stream, ops::user_launch((cudaStream_t)stream));
 }
 
 extern "C" int64_t dreamer_attn_kv4_workspace(const dreamer_kv4_cache *c, int n_heads) {
@@ -1565,5 +1565,5 @@ extern "C" int dreamer_attn_kv4(const dreamer_kv4_cache *c, const void *q, int64
   const int64_t need = ops::kv4_attn_workspace(to_cache(c), n_heads);
   if (need > 0 && (!workspace || !al16(workspace) || workspace_bytes < need)) return DREAMER_ERR_ARG;
   return ops::kv4_attn(to_cache(c), ops::Kv4Attn{q, ldq, out, ldo, lens, 0, n_heads, dtype, scale, workspace, status},
-                       (cudaStream_t)stream);
+                       (cudaStream_t)stream, ops::user_launch((cudaStream_t)stream));
 }

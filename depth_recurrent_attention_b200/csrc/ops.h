@@ -12,11 +12,20 @@
 namespace dreamer {
 namespace ops {
 
-// Launch options of a handle's path: programmatic dependent launch (the previous operation on
-// the stream is a kernel that the launched one waits for itself).
+// Launch options: programmatic dependent launch (the kernel waits by itself for what ran before on
+// the stream, so its blocks may be placed meanwhile).
 struct LaunchOpt {
   bool pdl = false;
 };
+// of a call on a user's stream: programmatic unless the stream is being captured, where the edge from
+// an operation that is no kernel could not be
+inline LaunchOpt user_launch(cudaStream_t s) {
+  cudaStreamCaptureStatus st;
+  LaunchOpt o;
+  if (cudaStreamIsCapturing(s, &st) == cudaSuccess) o.pdl = st == cudaStreamCaptureStatusNone;
+  else cudaGetLastError();
+  return o;
+}
 
 // Launch of one kernel (a template argument, so that what is noted of it is its own).  Its limit of
 // dynamic shared memory is raised once a device, noted in bit d of `raised`, and again where a launch

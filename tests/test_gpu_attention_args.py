@@ -176,3 +176,42 @@ def test_new_memory_belongs_to_the_stream_of_the_call(cuda):
         again = [torch.empty((6, 4, 64), dtype=torch.bfloat16, device="cuda") for _ in range(64)]
     assert p in [t.data_ptr() for t in again]
     s.synchronize()
+
+
+def test_calls_wait_for_what_runs_before_them(cuda):
+    """Inputs that a kernel, a copy or a fill writes just before the call, and outputs that a kernel still
+    reads, with no synchronisation between: the same bits as with one after every step."""
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache, attn_packed
+    g = torch.Generator("cuda").manual_seed(5)
+    z = dict(device="cuda", generator=g)
+    rows = [torch.randn((700, 4, 64), **z).bfloat16() for _ in range(3)]
+    host = torch.randn((3, 8, 64), generator=torch.Generator().manual_seed(6)).bfloat16().pin_memory()
+    cu, start, lens, heavy = _ints([0, 400, 401, 700]), _ints([0] * 3), _ints([400, 1, 299]), torch.randn((2048, 2048), **z)
+
+    def steps(sync):
+        c, got = KV4Cache.alloc(3, 4, 64, 64 * 80), []
+        x, q, o = torch.zeros_like(rows[0]), torch.zeros((3, 8, 64), dtype=torch.bfloat16, device="cuda"), None
+        for i in range(30):
+            h = heavy @ heavy                       # the stream is busy: what follows queues up
+            x.copy_(rows[i % 3])
+            x[i] += h[0, 0].bfloat16() * 0 + 1      # written by a kernel
+            sync()
+            c.store(x, x.flip(0), cu, start)
+            sync()
+            x.fill_(9)                              # after the store has read it
+            k, v = c.load(cu, start, 700)
+            sync()
+            o = attn_packed(k, v, k, cu, out=o)
+            got.append(o.float().sum((1, 2)) + k.float().sum((1, 2)))
+            sync()
+            q.copy_(host, non_blocking=True)        # by a copy engine
+            sync()
+            got.append(c.attend(q, lens))
+            q.zero_()
+            sync()
+        torch.cuda.synchronize()
+        return got
+
+    for a, b in zip(steps(lambda: None), steps(torch.cuda.synchronize)):
+        assert torch.equal(a, b)
