@@ -66,7 +66,8 @@ def attn_packed(q, k, v, cu_seqlens, out=None, scale=None, status=None, stream=N
     q [tokens][n_heads][dim], k and v [tokens][n_kv_heads][dim]; cu_seqlens int32 [prompts + 1],
     not decreasing: prompt i holds rows cu_seqlens[i] .. cu_seqlens[i+1]-1.  Query head j uses key
     head j // (n_heads // n_kv_heads); scale (positive) defaults to 1 / sqrt(dim).  Returns
-    `out`, [tokens][n_heads][dim]; rows of no prompt are not written.  bfloat16 takes dim 64 and
+    `out`, [tokens][n_heads][dim], which must not overlap q, k or v (it may be other columns of their
+    buffer); rows of no prompt are not written.  bfloat16 takes dim 64 and
     128, float32 also 16 and 32.  Boundaries out of order or outside the rows set `status`."""
     return _done(_ext.attn_packed(q, k, v, cu_seqlens, out, scale, status, stream), "dreamer_attn_packed")
 
@@ -116,7 +117,7 @@ class KV4Cache:
     def attend(self, q, lens, depth: int = 0, out=None, scale=None, status=None, stream=None):
         """Attention of one query token a sequence: q [batch][n_heads][dim] over the first
         lens[b] positions of sequence b (int32 [batch]; zeros where 0), query head j over key
-        head j // (n_heads // n_kv_heads).  Returns [batch][n_heads][dim]; scale defaults to
-        1 / sqrt(dim)."""
+        head j // (n_heads // n_kv_heads).  Returns [batch][n_heads][dim] (`out` may be q); scale
+        defaults to 1 / sqrt(dim)."""
         return _done(_ext.kv4_attend(self.data, self.head_dim, depth, q, lens, out, scale, status, stream),
                      "dreamer_attn_kv4")

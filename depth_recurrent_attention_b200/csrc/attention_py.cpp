@@ -69,6 +69,19 @@ Rows rows(const char *name, PyObject *o, int dev, int64_t heads = ANY, int64_t d
   return r;
 }
 
+// An output must not lie over an input; both may be columns of one buffer
+void apart(const char *name, const Rows &o, const Rows &x) {
+  if (o.n == 0 || x.n == 0) return;
+  const int64_t es = o.dtype ? 2 : 4, wo = o.h * o.d, wx = x.h * x.d;
+  const intptr_t o0 = (intptr_t)o.p, x0 = (intptr_t)x.p;
+  if (o0 + ((o.n - 1) * o.ld + wo) * es <= x0 || x0 + ((x.n - 1) * x.ld + wx) * es <= o0) return;
+  if (o.ld == x.ld && (x0 - o0) % es == 0) {
+    const int64_t c = ((x0 - o0) / es % o.ld + o.ld) % o.ld;  // x's first column from out's
+    if (c >= wo && c + wx <= o.ld) return;
+  }
+  refuse("out: overlaps %s", name);
+}
+
 int32_t *ints(const char *name, PyObject *o, int dev, int64_t n) {
   const at::Tensor &t = tensor(name, o);
   if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != at::kInt || t.dim() != 1 || t.size(0) != n ||
@@ -184,6 +197,9 @@ PyObject *attn_packed(PyObject *, PyObject *const *a, Py_ssize_t n) {
       o.ld = q.h * q.d;
     } else {
       o = rows("out", a[4], dev, q.h, q.d, q.dtype, q.n);
+      apart("q", o, q);
+      apart("k", o, k);
+      apart("v", o, v);
     }
     const int rc = q.n ? unlocked<dreamer_attn_packed>(q.p, q.ld, k.p, k.ld, v.p, v.ld, o.p, o.ld, cu, (int)tc.numel() - 1,
                                              (int)q.n, (int)q.h, (int)k.h, (int)q.d, q.dtype, scale, status, at.stream)
@@ -267,6 +283,7 @@ PyObject *kv4_load(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       k = rows("out[0]", a[7], c.dev, h, d, dtype, rows_n);
       v = rows("out[1]", a[8], c.dev, h, d, dtype, rows_n);
+      apart("out[1]", k, v);
     }
     const int rc = rows_n ? unlocked<dreamer_kv4_load>(&c.c, k.p, k.ld, v.p, v.ld, cu, start, (int)rows_n, dtype, mine, status, at.stream) : 0;
     if (rc) return PyLong_FromLong(rc);
@@ -292,6 +309,7 @@ PyObject *kv4_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
       o.ld = q.h * q.d;
     } else {
       o = rows("out", a[5], c.dev, q.h, q.d, q.dtype, q.n);
+      if (o.p != q.p || o.ld != q.ld) apart("q", o, q);  // out may be q itself
     }
     const int64_t need = dreamer_attn_kv4_workspace(&c.c, (int)q.h);
     if (need) ws = at.memory({need}, at::kByte);  // returned to the stream's pool at the end

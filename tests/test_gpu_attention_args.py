@@ -59,6 +59,28 @@ def test_attn_packed_refuses(cuda, what):
         attn_packed(**_args(**BAD_PACKED[what](torch)))
 
 
+def test_out_beside_its_inputs_but_not_over_them(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    buf = torch.randn((50, 4 + 2 + 2 + 4, 64), device="cuda").bfloat16()
+    q, k, v, out, cu = buf[:, :4], buf[:, 4:6], buf[:, 6:8], buf[:, 8:], _ints([0, 20, 50])
+    want = attn_packed(q.clone(), k.clone(), v.clone(), cu)
+    assert torch.equal(attn_packed(q, k, v, cu, out=out), want) and torch.equal(out, want)
+    for bad in (q, buf[:, 1:5], buf[:, 4:8], buf[:, 5:9], buf[:, 7:11]):
+        with pytest.raises(ValueError):
+            attn_packed(q, k, v, cu, out=bad)
+    rows = torch.randn((99, 4, 64), device="cuda").bfloat16()       # rows of one buffer
+    one = _ints([0, 33])
+    attn_packed(rows[:33], rows[33:66], rows[33:66], one, out=rows[66:])
+    for first in (0, 1, 33, 65):
+        with pytest.raises(ValueError):
+            attn_packed(rows[:33], rows[33:66], rows[33:66], one, out=rows[first:first + 33])
+    flat = torch.randn(40 * 320, device="cuda").bfloat16()          # strides that differ
+    with pytest.raises(ValueError):
+        attn_packed(q[:20], k[:20], v[:20], _ints([0, 20]), out=buf.view(-1)[:20 * 256].view(20, 4, 64))
+    assert attn_packed(q[:20], k[:20], v[:20], _ints([0, 20]), out=flat[:20 * 256].view(20, 4, 64)).shape == (20, 4, 64)
+
+
 def test_other_types_and_unsupported_dims(cuda):
     import torch
     from depth_recurrent_attention_b200.attention import attn_packed
@@ -113,8 +135,23 @@ def test_the_cache_refuses(cuda):
     refused(c.attend, q, cu)
     refused(c.attend, q, lens, out=q[:, :2])
     refused(c.attend, q, lens, scale=float("inf"))
+    wide = torch.ones((2, 6, 64), **z)
+    refused(c.attend, wide[:, :4], lens, out=wide[:, 2:])
+    refused(c.load, cu, start, 5, out=(k, k))
     refused(c.attend, q, lens, status=torch.zeros(1, device="cuda"))
     assert not c.data.any()                      # nothing was written
+
+
+def test_attend_in_place(cuda):
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    for cap in (64, 64 * 200):                  # one launch, and a split with a join
+        c = KV4Cache.alloc(2, 2, 64, cap)
+        k = torch.randn((100, 2, 64), device="cuda").bfloat16()
+        c.store(k, k.flip(0), _ints([0, 60, 100]), _ints([0, 0]))
+        q = torch.randn((2, 4, 64), device="cuda").bfloat16()
+        want = c.attend(q, _ints([60, 40]))
+        assert c.attend(q, _ints([60, 40]), out=q) is q and torch.equal(q, want)
 
 
 def test_no_rows(cuda):
