@@ -101,6 +101,31 @@ def test_packed_against_64_bits(cuda, dtype, d, lens, Hq, Hk):
     _check(_f64(out), want, tol, np.ones(sum(lens), bool))
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 32)])
+@pytest.mark.parametrize("n,longest,first", [(64, 9, 0), (65, 9, 0), (65, 300, 150), (1100, 4, 1), (3000, 2, 700)])
+def test_many_prompts(cuda, dtype, d, n, longest, first):
+    """As many prompts as change how a block finds its item, empty ones among them, rows of no prompt
+    before and behind them."""
+    import torch
+    from depth_recurrent_attention_b200.attention import attn_packed
+    rng = np.random.default_rng(n + longest)
+    lens = rng.integers(0, longest + 1, n)
+    cu = first + np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1]) + 5
+    q, k, v = _qkv(rng, T, 2, 1, d, dtype)
+    out, st = torch.full_like(q, 3.0), _ints([0])
+    attn_packed(q, k, v, _ints(cu), out=out, status=st)
+    want, tol = reference(_f64(q), _f64(k), _f64(v), cu, d ** -0.5, dtype)
+    written = np.zeros(T, bool)
+    written[first:T - 5] = True
+    _check(_f64(out), want, tol, written)
+    assert (out[~torch.from_numpy(written).cuda()] == 3).all() and st.item() == 0
+    bad = cu.copy()
+    bad[n // 2] = cu[-1] + 9                     # past the rows, and decreasing behind
+    attn_packed(q, k, v, _ints(bad), out=out, status=st)
+    assert st.item() != 0 and (out[:first] == 3).all()
+
+
 @pytest.mark.parametrize("d", [16, 32, 64, 128])
 @pytest.mark.parametrize("Hq", [2, 24])       # few items with long rows, and many: two ways to share a row's keys
 def test_float32_of_few_and_of_many_items(cuda, Hq, d):
