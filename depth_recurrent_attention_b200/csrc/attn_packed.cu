@@ -220,10 +220,6 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % a.Hq;
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), C::COLS);
-    tmem_relinquish();
-  }
   if (threadIdx.x == 64) {
     mbar_init(smem_u32(q_full), 1);
     for (int s = 0; s < KST; s++) {
@@ -248,6 +244,11 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
     prefetch_tmap(&tmv);
   }
   pdl_wait();  // inputs of the previous kernel are visible from here on
+  // tensor memory only now: a kernel before, of whatever origin, may have to allocate its own yet
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::COLS);
+    tmem_relinquish();
+  }
   if (warp == 0) {
     if (blockIdx.x == 0) check_cu(a);
     const int3 it = find_item<128 * TILES>(a, blockIdx.x / a.Hq);
