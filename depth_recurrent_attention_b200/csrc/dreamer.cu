@@ -1568,6 +1568,11 @@ extern "C" int dreamer_test_inject(dreamer_handle *h, int what) {
   h->inject_skip = what;
   return DREAMER_OK;
 }
+// The next attention operator (ops.h) withholds one copy of one warp, and its wait runs out.
+extern "C" int dreamer_test_withhold(int cta, int warp, int copy) {
+  ops::withheld = ops::Withhold{cta, warp, copy};
+  return DREAMER_OK;
+}
 #endif
 
 extern "C" int dreamer_bias_update_counts(dreamer_handle *h, float lambda, const int32_t *counts,

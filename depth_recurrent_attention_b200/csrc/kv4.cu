@@ -375,6 +375,9 @@ struct AttnArgs {
   int *err;
   float *part;   // split form: [slot][GP][D + 4] partial outputs, maximum, sum
   int n_warps;   // split form: warps of the grid
+#ifdef DREAMER_TEST_HOOKS
+  Withhold withhold;
+#endif
 };
 
 __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
@@ -845,18 +848,23 @@ struct WarpAttn {
   }
 };
 
-// Ring of a warp's blocks in shared memory: blocks first, first + stride, ... (n of them) of a run
-// that starts at base.
+// Ring of a warp's blocks in shared memory.  wait() answers the same in every lane: what follows it is
+// done by whole warps, and at the limit the lanes' own answers may differ (one more look each).
 template <int BLK, int ST>
 struct Ring {
   uint8_t *mem;
   uint64_t *bars;
   volatile int *abort;
   int *err;
-  uint32_t at = 0;   // blocks taken since the barriers were made
+#ifdef DREAMER_TEST_HOOKS
+  int withhold = -1;  // this copy is announced and never made
+#endif
   __device__ __forceinline__ void issue(uint32_t i, const uint8_t *src) const {
     const uint32_t bar = tc::smem_u32(&bars[i % ST]);
     tc::mbar_expect_tx(bar, BLK);
+#ifdef DREAMER_TEST_HOOKS
+    if ((int)i == withhold) return;
+#endif
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
             tc::smem_u32(mem + (i % ST) * BLK)),
@@ -864,7 +872,7 @@ struct Ring {
         : "memory");
   }
   __device__ __forceinline__ bool wait(uint32_t i) const {
-    return tc::mbar_wait(tc::smem_u32(&bars[i % ST]), (i / ST) & 1, abort, err);
+    return __all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&bars[i % ST]), (i / ST) & 1, abort, err));
   }
   // after an expired wait: the copies i0 .. i1 - 1, still in flight, land (or time out) before the exit
   __device__ __forceinline__ void drain(uint32_t i0, uint32_t i1) const {
@@ -938,14 +946,19 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
   const uint8_t *base = a.data + (long)pair * (a.cap / KV4_BLOCK) * BLK;
   const int mine = blk1 - blk0 > warp ? (blk1 - blk0 - warp + NW - 1) / NW : 0;
   Ring<BLK, ST> ring{ring_mem + warp * ST * BLK, bars + warp * ST, &s_abort, a.err};
+#ifdef DREAMER_TEST_HOOKS
+  ring.withhold = a.withhold.copy_of(blockIdx.x, warp);
+#endif
   auto src = [&](int i) { return base + (long)(blk0 + warp + i * NW) * BLK; };
   if (lane == 0)
     for (int i = 0; i < ST && i < mine; i++) ring.issue(i, src(i));
   W w;
   w.start(reinterpret_cast<const T *>(a.q) + (long)b * a.ldq + (long)head0 * D, nq, a.scale_log2);
+  bool expired = false;
   for (int i = 0; i < mine; i++) {
     if (!ring.wait(i)) {
       if (lane == 0) ring.drain(i, min(mine, i + ST));
+      expired = true;
       break;
     }
     w.block(ring.mem + (i % ST) * BLK, (blk0 + warp + i * NW) * KV4_BLOCK, nkeys);
@@ -953,6 +966,7 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
     if (lane == 0 && i + ST < mine) ring.issue(i + ST, src(i + ST));  // into the stage just read
   }
   w.join();
+  if (expired) w.l2[0] = w.l2[1] = NAN;  // the item's sum, and so its output in every CTA of the cluster
   __syncthreads();  // every warp is done with the rings
   float *part = reinterpret_cast<float *>(ring_mem);
   if (2 * t < GP) {
@@ -992,7 +1006,6 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
   // every CTA of the cluster writes its share of the output
   if (csize > 1) cluster_sync();
   else __syncthreads();
-  const int aborted = *(volatile int *)&s_abort;
   for (int e = (int)crank * (NW * 32) + threadIdx.x; e < nq * D; e += (int)csize * (NW * 32)) {
     const int qh = e / D;
     float acc = 0.f, l = 0.f;
@@ -1011,8 +1024,7 @@ __global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
       l = sL[qh];
     }
     const float res = nkeys == 0 ? 0.f : acc / l;
-    if (!aborted)
-      reinterpret_cast<T *>(a.out)[(long)b * a.ldo + (long)(head0 + qh) * D + e % D] = from_f<T>(res);
+    reinterpret_cast<T *>(a.out)[(long)b * a.ldo + (long)(head0 + qh) * D + e % D] = from_f<T>(res);
   }
   if (csize > 1) cluster_sync();  // shared memory that others read stays until they have
 }
@@ -1101,6 +1113,9 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
   int v = max(f0, first), blk = v - first;
   one = first <= c0 && c1 <= first + nb && per < nb;
   Ring<BLK, ST> ring{ring_mem + warp * ST * BLK, bars + warp * ST, &s_abort, a.err};
+#ifdef DREAMER_TEST_HOOKS
+  ring.withhold = a.withhold.copy_of(blockIdx.x, warp);
+#endif
   int issued = 0, ld_v = v, ld_b = b, ld_it = it, ld_nb = nb, ld_left = nb - blk;
   const uint8_t *ld = a.data + ((long)(b * a.Hkv + it / a.qchunks) * cap_blk + blk) * BLK;
   auto issue_next = [&]() {
@@ -1121,16 +1136,17 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
   };
   for (int i = 0; i < ST && ld_v < f1; i++) issue_next();
   W w;
+  bool expired = false;  // a wait was: this and the run's further items become NaN
   for (int i = 0; v < f1;) {  // segments of one item each
     const int kvh = it / a.qchunks, qc = it % a.qchunks;
     const int head0 = kvh * a.G + qc * GP, nq = min(GP, a.G - qc * GP);
     const int nkeys = keys_of(a, b, false);
     const int take = min(nb - blk, f1 - v);
     w.start(reinterpret_cast<const T *>(a.q) + (long)b * a.ldq + (long)head0 * D, nq, a.scale_log2);
-    for (int k = 0; k < take; k++, i++) {
+    for (int k = 0; k < take && !expired; k++, i++) {
       if (!ring.wait(i)) {
         if (lane == 0) ring.drain(i, issued);
-        v = f1;
+        expired = true;
         break;
       }
       w.block(ring.mem + (i % ST) * BLK, (blk + k) * KV4_BLOCK, nkeys);
@@ -1138,6 +1154,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) kv4_split_kernel(AttnArgs a) {
       if (ld_v < f1) issue_next();  // into the stage just read
     }
     w.join();
+    if (expired) w.l2[0] = w.l2[1] = NAN;
     if (2 * t < GP) {
       if (one) {  // into the warp's own stages, all read
         float *dst = reinterpret_cast<float *>(ring.mem);
@@ -1464,6 +1481,9 @@ int kv4_attn(const Kv4Cache &c, const Kv4Attn &t, cudaStream_t s, LaunchOpt o) {
   a.scale_log2 = t.scale * 1.4426950408889634f;
   a.err = t.err;
   a.part = (float *)t.workspace;
+#ifdef DREAMER_TEST_HOOKS
+  a.withhold = take_withhold();
+#endif
   if (c.d == 64) return t.dtype == 0 ? dispatch_attn<float, 1>(a, s, o) : dispatch_attn<bf16, 1>(a, s, o);
   return t.dtype == 0 ? dispatch_attn<float, 2>(a, s, o) : dispatch_attn<bf16, 2>(a, s, o);
 }

@@ -12,6 +12,21 @@
 namespace dreamer {
 namespace ops {
 
+#ifdef DREAMER_TEST_HOOKS
+// One copy into shared memory that the next attention kernel announces and never makes, so that the
+// wait for it runs out: copy number `copy` of a warp of a CTA.
+struct Withhold {
+  int cta, warp, copy;
+  __device__ int copy_of(unsigned c, int w) const { return (int)c == cta && w == warp ? copy : -1; }
+};
+inline Withhold withheld{-1, -1, -1};
+inline Withhold take_withhold() {
+  const Withhold w = withheld;
+  withheld = Withhold{-1, -1, -1};
+  return w;
+}
+#endif
+
 // Launch options: programmatic dependent launch (the kernel waits by itself for what ran before on
 // the stream, so its blocks may be placed meanwhile).
 struct LaunchOpt {

@@ -285,6 +285,7 @@ int dreamer_kv4_load(const dreamer_kv4_cache *cache, void *k, int64_t ldk, void 
  * are float32; bfloat16 takes q, and a 64-token block's weights, as 16-bit fixed-point numbers of
  * their largest (of 64 channels; of the block), float32 works to float32 precision throughout.
  * What lies in the cache behind lens[b] is not used.
+ * After an expired wait (status) the outputs that wanted the missing keys are NaN.
  * workspace: device memory of at least dreamer_attn_kv4_workspace() bytes (NULL where that is 0),
  * 16-byte aligned, contents of no matter; calls that may run at the same time need one each.  */
 int dreamer_attn_kv4(const dreamer_kv4_cache *cache, const void *q, int64_t ldq, void *out,
