@@ -41,6 +41,9 @@ struct PackedArgs {
   const int *out_rows;    // output row of token t, or null: t
   float scale_log2;
   int *err;
+#ifdef DREAMER_TEST_HOOKS
+  Withhold withhold;      // of the K (warp 0) or V (warp 2) blocks
+#endif
 };
 
 // First row and length of prompt i; boundaries outside 0 .. n_tokens or decreasing are cut.
@@ -213,7 +216,8 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
   uint64_t *v_full = k_empty + KST, *v_empty = v_full + VST;
   // per tile: scores ready; SEP: scores in registers; weights ready; SEP: output product done
   uint64_t *s_full = v_empty + VST, *s_read = s_full + 2, *p_full = s_read + 2, *pv_done = p_full + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pv_done + 2);
+  uint64_t *drained = pv_done + 2;  // after an expired wait: no product is in flight
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *item_slot = reinterpret_cast<int *>(tmem_slot + 2);          // row0, length, tile
   volatile int *by_rows = reinterpret_cast<volatile int *>(tmem_slot + 5);  // [2] diagonal block on CUDA cores
@@ -237,6 +241,7 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
       mbar_init(smem_u32(&pv_done[i]), 1);
       by_rows[i] = 0;
     }
+    mbar_init(smem_u32(drained), 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmq);
@@ -294,30 +299,31 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
         uint64_t *fullb = isK ? k_full : v_full, *emptyb = isK ? k_empty : v_empty;
         uint8_t *ring = isK ? sK : sV;
         int issued_ph[4] = {-1, -1, -1, -1};
-        bool ok = true;
         for (int j = 0; j < nb; j++) {
           const int s = j % NS;
           const uint32_t ph = (j / NS) & 1;
-          if (!mbar_wait(smem_u32(&emptyb[s]), ph ^ 1, abort_flag, a.err)) { ok = false; break; }
+          if (!mbar_wait(smem_u32(&emptyb[s]), ph ^ 1, abort_flag, a.err)) break;
           mbar_expect_tx(smem_u32(&fullb[s]), C::KV_BYTES);
+#ifdef DREAMER_TEST_HOOKS
+          if (j == a.withhold.copy_of(blockIdx.x, warp)) continue;
+#endif
           for (int c = 0; c < CH; c++)
             tma_load_2d(smem_u32(ring + s * C::KV_BYTES + c * C::TILE), tm, smem_u32(&fullb[s]),
                         colb + 64 * c, row0 + j * 128);
           issued_ph[s] = (int)ph;
         }
-        // every copy issued lands before the CTA can exit
+        // every copy issued lands before the CTA can exit, also where another warp gave up waiting
         const uint64_t t0 = globaltimer();
         if (isK)
           while (!mbar_try_wait(smem_u32(q_full), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
           }
-        if (!ok)
-          for (int i = 0; i < NS; i++)
-            if (issued_ph[i] >= 0) {
-              const uint64_t t1 = globaltimer();
-              while (!mbar_try_wait(smem_u32(&fullb[i]), (uint32_t)issued_ph[i]) &&
-                     globaltimer() - t1 < WAIT_LIMIT_NS) {
-              }
+        for (int i = 0; i < NS; i++)
+          if (issued_ph[i] >= 0) {
+            const uint64_t t1 = globaltimer();
+            while (!mbar_try_wait(smem_u32(&fullb[i]), (uint32_t)issued_ph[i]) &&
+                   globaltimer() - t1 < WAIT_LIMIT_NS) {
             }
+          }
       }
     } else if (warp == 1) {
       // ------------------------------------------------- MMA issuer
@@ -371,7 +377,8 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
         commit(&k_empty[0]);
       }
       int vs = 0, ks = 1 % KST;  // stages of block j's values and of block j + 1's keys
-      for (int j = 0; j < un && ok; j++) {
+      int j = 0;
+      for (; j < un && ok; j++) {
         const bool next = j + 1 < un;
         if (SEP && next) {
           if (!wait(&k_full[ks], (j + 1) / KST)) break;
@@ -400,6 +407,12 @@ __global__ void __launch_bounds__(PkCfg<D>::THREADS, PkCfg<D>::CTAS)
         if (!SEP && next) commit(&k_empty[ks]);
         if (++vs == VST) vs = 0;
         if (++ks == KST) ks = 0;
+      }
+      if (j < un || !ok) {  // gave up: the products issued end before tensor memory is given back
+        commit(drained);
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(smem_u32(drained), 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+        }
       }
     }
   } else {
@@ -904,6 +917,9 @@ int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
   a.out = p.out; a.ldo = p.ldo; a.out_rows = p.out_rows;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.err = p.err;
+#ifdef DREAMER_TEST_HOOKS
+  a.withhold = take_withhold();
+#endif
   if (p.n_tokens == 0 || p.n_seq == 0) return DREAMER_OK;
   if (p.dtype == 1) {
     CUtensorMap tq, tk, tv;

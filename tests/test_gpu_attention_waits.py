@@ -21,6 +21,7 @@ def hooks(cuda):
     L.dreamer_attn_kv4.argtypes = [vp, vp, i64, vp, i64, vp, i, i, f, vp, i64, vp, vp]
     L.dreamer_attn_kv4_workspace.argtypes = [vp, i]
     L.dreamer_attn_kv4_workspace.restype = i64
+    L.dreamer_attn_packed.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i, i, i, i, i, i, f, vp, vp]
     L.dreamer_test_withhold.argtypes = [i, i, i]
     return L
 
@@ -84,4 +85,41 @@ def test_attend_after_an_expired_wait(hooks, dtype, lens, H, capacity, at):
     assert torch.equal(out[~lost], good[~lost])
     st.zero_()
     _attend(hooks, c, q, ln, out, st)
+    assert st.item() == 0 and torch.equal(out, good)
+
+
+@pytest.mark.parametrize("d,at", [
+    (64, (0, 0, 0)), (64, (0, 0, 1)), (64, (1, 0, 2)),      # keys of the longest tile: its first, a later, its last block
+    (64, (0, 2, 0)), (64, (1, 2, 2)),                       # values
+    (128, (0, 0, 0)), (128, (1, 0, 2)), (128, (0, 2, 1)),   # a block of one tile of the pair
+    (128, (2, 0, 1)), (128, (3, 2, 1)), (128, (2, 2, 0)),   # a pair of tiles: the second's last block, both tiles' first
+])
+def test_packed_after_an_expired_wait(hooks, d, at):
+    """Rows of the block that gave up are right or left as they were; all others are right."""
+    import torch
+    torch.manual_seed(4)
+    lens, Hq = [300, 77], 2
+    T = sum(lens)
+    q = torch.randn((T, Hq, d), device="cuda").bfloat16()
+    k, v = torch.randn((2, T, 1, d), device="cuda").bfloat16()
+    cu, st = _ints([0, 300, 377]), _ints([0])
+    good, out = torch.empty_like(q), torch.full_like(q, 5.0)
+
+    def run(o):
+        rc = hooks.dreamer_attn_packed(q.data_ptr(), Hq * d, k.data_ptr(), d, v.data_ptr(), d, o.data_ptr(), Hq * d,
+                                       cu.data_ptr(), 2, T, Hq, 1, d, 1, d ** -0.5, st.data_ptr(), None)
+        assert rc == 0
+        torch.cuda.synchronize()
+
+    run(good)
+    assert st.item() == 0
+    hooks.dreamer_test_withhold(*at)
+    run(out)
+    assert st.item() == TIMEOUT
+    left = (out == 5.0).all(-1)
+    assert 1 <= int(left.sum()) <= (256 if d == 128 else 128)
+    assert torch.equal(out[~left], good[~left])
+    st.zero_()
+    for _ in range(3):                                   # tensor memory was given back
+        run(out)
     assert st.item() == 0 and torch.equal(out, good)
