@@ -1011,10 +1011,11 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
       ops::Kv4Rows r4{};
       r4.k = kv; r4.v = kv + hd; r4.ldk = r4.ldv = 3 * hd;
       r4.start = io.cache_len; r4.n_rows = n; r4.dtype = c.dtype; r4.err = h->err;
+      r4.limit = c.max_cache_len;  // as the projection's epilogue: a refused position is not written
       ops::Kv4Attn a4{};
       a4.q = h->qkv_sa; a4.ldq = 3 * hd; a4.out = h->attn; a4.ldo = 2 * hd;
       a4.lens = io.cache_len; a4.len_add = 1; a4.Hq = c.n_heads; a4.dtype = c.dtype;
-      a4.scale = 1.0f / sqrtf((float)d); a4.workspace = h->kv4_ws; a4.err = h->err;
+      a4.scale = 1.0f / sqrtf((float)d); a4.workspace = h->kv4_ws; a4.err = h->err; a4.limit = c.max_cache_len;
       ops::LaunchOpt o;
       o.pdl = pdl_take(h, st);
       if (ops::kv4_store(c4, r4, st, o) != DREAMER_OK) h->path_err = 1;

@@ -45,6 +45,7 @@ constexpr int CU_SMEM = 1024;  // boundaries searched in shared memory up to thi
 struct RowArgs {
   uint8_t *data;
   int B, Hkv, ng, cap;
+  int limit;      // positions that may be used
   const void *k, *v;
   long ldk, ldv;
   const int *cu, *start;
@@ -55,7 +56,7 @@ struct RowArgs {
 
 // Place in the cache of the CTA's rows: byte offset of a row's codes in head 0's plane 0, and of its
 // pair from there on.  Row r belongs to the sequence b with cu[b] <= r < cu[b + 1]; an offset below 0: the
-// row is in no sequence, or its position is outside the cache (reported).
+// row is in no sequence, or its position is outside 0 .. limit - 1 (reported).
 struct Place {
   long codes;
   int pair;
@@ -89,7 +90,7 @@ __device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu,
       }
       if (b >= 0) {
         const long q = (long)a.start[b] + off;
-        if (q >= 0 && q < a.cap) p = (int)q;
+        if (q >= 0 && q < a.limit) p = (int)q;
         else raise_dev_error(a.err, DEV_BAD_INDEX);
       }
     }
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
 struct AttnArgs {
   const uint8_t *data;
   int B, Hkv, cap, Hq, G, qchunks;
+  int limit;     // keys that a sequence may have
   const void *q;
   long ldq;
   void *out;
@@ -885,10 +887,10 @@ struct Ring {
   }
 };
 
-// Keys of sequence b; a length outside the cache is reported and counts as none
+// Keys of sequence b; a length outside 0 .. limit is reported and counts as none
 __device__ __forceinline__ int keys_of(const AttnArgs &a, int b, bool report) {
   const long len = (long)a.lens[b] + a.len_add;
-  if (len < 0 || len > a.cap) {
+  if (len < 0 || len > a.limit) {
     if (report) raise_dev_error(a.err, DEV_BAD_INDEX);
     return 0;
   }
@@ -1359,6 +1361,7 @@ RowArgs row_args(const Kv4Cache &c, const Kv4Rows &r) {
   a.B = c.B; a.Hkv = c.Hkv; a.ng = c.d / KV4_GROUP; a.cap = c.cap;
   a.k = r.k; a.v = r.v; a.ldk = r.ldk; a.ldv = r.ldv;
   a.cu = r.cu; a.start = r.start; a.n_rows = r.n_rows; a.zero_rest = r.zero_rest; a.err = r.err;
+  a.limit = r.limit ? r.limit : c.cap;
   return a;
 }
 dim3 row_grid(const RowArgs &a, int rows) {
@@ -1478,6 +1481,7 @@ int kv4_attn(const Kv4Cache &c, const Kv4Attn &t, cudaStream_t s, LaunchOpt o) {
   a.B = c.B; a.Hkv = c.Hkv; a.cap = c.cap; a.Hq = t.Hq; a.G = t.Hq / c.Hkv;
   a.q = t.q; a.ldq = t.ldq; a.out = t.out; a.ldo = t.ldo;
   a.lens = t.lens; a.len_add = t.len_add;
+  a.limit = t.limit ? t.limit : c.cap;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   a.err = t.err;
   a.part = (float *)t.workspace;
@@ -1551,7 +1555,7 @@ extern "C" int dreamer_kv4_store(const dreamer_kv4_cache *c, const void *k, int6
                                  int dtype, int32_t *status, dreamer_stream stream) {
   const int rc = check_rows(c, k, ldk, v, ldv, cu_rows, start, n_rows, dtype);
   if (rc) return rc;
-  return ops::kv4_store(to_cache(c), ops::Kv4Rows{k, v, ldk, ldv, cu_rows, start, n_rows, dtype, 0, status},
+  return ops::kv4_store(to_cache(c), ops::Kv4Rows{k, v, ldk, ldv, cu_rows, start, n_rows, dtype, 0, status, 0},
                         (cudaStream_t)stream, ops::user_launch((cudaStream_t)stream));
 }
 
@@ -1560,7 +1564,7 @@ extern "C" int dreamer_kv4_load(const dreamer_kv4_cache *c, void *k, int64_t ldk
                                 int zero_rest, int32_t *status, dreamer_stream stream) {
   const int rc = check_rows(c, k, ldk, v, ldv, cu_rows, start, n_rows, dtype);
   if (rc) return rc;
-  return ops::kv4_load(to_cache(c), ops::Kv4Rows{k, v, ldk, ldv, cu_rows, start, n_rows, dtype, zero_rest ? 1 : 0, status},
+  return ops::kv4_load(to_cache(c), ops::Kv4Rows{k, v, ldk, ldv, cu_rows, start, n_rows, dtype, zero_rest ? 1 : 0, status, 0},
                        (cudaStream_t)stream, ops::user_launch((cudaStream_t)stream));
 }
 
@@ -1584,6 +1588,6 @@ extern "C" int dreamer_attn_kv4(const dreamer_kv4_cache *c, const void *q, int64
   if (!al16(q) || !al16(out) || ldq < w || ldo < w || (ldq * es) % 16 || (ldo * es) % 16) return DREAMER_ERR_ARG;
   const int64_t need = ops::kv4_attn_workspace(to_cache(c), n_heads);
   if (need > 0 && (!workspace || !al16(workspace) || workspace_bytes < need)) return DREAMER_ERR_ARG;
-  return ops::kv4_attn(to_cache(c), ops::Kv4Attn{q, ldq, out, ldo, lens, 0, n_heads, dtype, scale, workspace, status},
+  return ops::kv4_attn(to_cache(c), ops::Kv4Attn{q, ldq, out, ldo, lens, 0, n_heads, dtype, scale, workspace, status, 0},
                        (cudaStream_t)stream, ops::user_launch((cudaStream_t)stream));
 }

@@ -130,6 +130,7 @@ struct Kv4Rows {
   int dtype;          // 0 float32, 1 bfloat16
   int zero_rest;      // load: rows of no sequence become zeros
   int *err;           // device error flag or null
+  int limit;          // positions from here on are refused (0: from the capacity on)
 };
 int kv4_store(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o = LaunchOpt());
 int kv4_load(const Kv4Cache &c, const Kv4Rows &r, cudaStream_t s, LaunchOpt o = LaunchOpt());
@@ -146,6 +147,7 @@ struct Kv4Attn {
   float scale;
   void *workspace;  // kv4_attn_workspace bytes
   int *err;
+  int limit;        // more keys than this are refused (0: than the capacity)
 };
 // bytes of the workspace (0: none needed); any_capacity: whatever c.cap is
 long kv4_attn_workspace(const Kv4Cache &c, int Hq, bool any_capacity = false);

@@ -313,7 +313,8 @@ int dreamer_core_forward_packed(dreamer_handle *h, const void *x_in, void *x_out
 /* dreamer_decode_step over 4-bit caches: cache->data holds the depths' caches one behind the
  * other ([L] of dreamer_kv4_bytes() each), batch, n_kv_heads = n_heads and head_dim those of the
  * handle, capacity at least max_cache_len.  Each depth quantises the new token's key and value
- * into position cache_len[b] (< max_cache_len) and attends cache_len[b] + 1 positions.       */
+ * into position cache_len[b] (< max_cache_len) and attends cache_len[b] + 1 positions.  Another
+ * position is reported by the next call; nothing of that sequence is stored.                */
 int dreamer_decode_step_kv4(dreamer_handle *h, const void *x_new, const dreamer_kv4_cache *cache,
                             const int32_t *cache_len, void *x_out, const dreamer_trace *trace,
                             dreamer_stream stream);
