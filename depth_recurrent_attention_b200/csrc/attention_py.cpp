@@ -271,7 +271,7 @@ PyObject *kv4_load(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int32_t *status = status_of(a[9], c.dev);
     Place at(a[10], c.dev);
     const int64_t h = c.c.n_kv_heads, d = c.c.head_dim;
-    const bool mine = a[7] == Py_None;
+    const bool mine = a[7] == Py_None && a[8] == Py_None;  // half a pair is refused below
     at::Tensor tk, tv;
     Rows k, v;
     if (mine) {
