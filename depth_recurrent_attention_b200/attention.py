@@ -76,7 +76,8 @@ class KV4Cache:
     """A 4-bit cache of keys and values for `batch` sequences, at `depth` depths.
 
     data: uint8 [depth][batch][n_kv_heads][capacity / 64][block bytes] (KV4Cache.alloc makes
-    one); the layout of a block and the number format are those of dreamer_kv4_cache."""
+    one); the layout of a block and the number format are those of dreamer_kv4_cache.  Outputs, and
+    rows to be stored, must not lie in the cache's own memory."""
 
     def __init__(self, data, head_dim: int):
         self.depth, self.batch, self.n_kv_heads, self.capacity = _ext.kv4_sizes(data, head_dim)

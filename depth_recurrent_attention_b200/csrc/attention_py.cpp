@@ -213,6 +213,7 @@ struct Cache {
   dreamer_kv4_cache c;
   int dev;
   int64_t depth;
+  intptr_t begin, end;  // bytes of all depths
 };
 Cache cache_of(PyObject *data, PyObject *head_dim, PyObject *depth) {
   const at::Tensor &t = tensor("data", data);
@@ -229,12 +230,21 @@ Cache cache_of(PyObject *data, PyObject *head_dim, PyObject *depth) {
   c.depth = t.size(0);
   const int64_t l = depth ? whole(depth) : 0;
   if (l < 0 || l >= c.depth) refuse("depth: 0..%lld", (long long)c.depth - 1);
+  c.begin = (intptr_t)t.data_ptr();
+  c.end = c.begin + (intptr_t)t.numel();
   c.c.data = (uint8_t *)t.data_ptr() + l * t.stride(0);
   c.c.batch = (int)t.size(1);
   c.c.n_kv_heads = (int)t.size(2);
   c.c.head_dim = (int)d;
   c.c.capacity = (int)t.size(3) * 64;
   return c;
+}
+
+// Rows that the cache must not hold: outputs, and what is stored into it
+void off_cache(const char *name, const Rows &x, const Cache &c) {
+  if (x.n == 0) return;
+  const intptr_t x0 = (intptr_t)x.p, x1 = x0 + ((x.n - 1) * x.ld + x.h * x.d) * (x.dtype ? 2 : 4);
+  if (x0 < c.end && c.begin < x1) refuse("%s: overlaps the cache", name);
 }
 
 // kv4_sizes(data, head_dim) -> (depth, batch, heads, capacity)
@@ -252,6 +262,8 @@ PyObject *kv4_store(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Rows k = rows("k", a[3], c.dev, c.c.n_kv_heads, c.c.head_dim),
                v = rows("v", a[4], c.dev, k.h, k.d, k.dtype, k.n);
     const int32_t *cu = ints("cu_rows", a[5], c.dev, c.c.batch + 1LL), *start = ints("start", a[6], c.dev, c.c.batch);
+    off_cache("k", k, c);
+    off_cache("v", v, c);
     int32_t *status = status_of(a[7], c.dev);
     if (k.n >= (1LL << 31)) refuse("k: below 2^31 rows");
     Place at(a[8], c.dev);
@@ -284,6 +296,8 @@ PyObject *kv4_load(PyObject *, PyObject *const *a, Py_ssize_t n) {
       k = rows("out[0]", a[7], c.dev, h, d, dtype, rows_n);
       v = rows("out[1]", a[8], c.dev, h, d, dtype, rows_n);
       apart("out[1]", k, v);
+      off_cache("out[0]", k, c);
+      off_cache("out[1]", v, c);
     }
     const int rc = rows_n ? unlocked<dreamer_kv4_load>(&c.c, k.p, k.ld, v.p, v.ld, cu, start, (int)rows_n, dtype, mine, status, at.stream) : 0;
     if (rc) return PyLong_FromLong(rc);
@@ -310,6 +324,7 @@ PyObject *kv4_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       o = rows("out", a[5], c.dev, q.h, q.d, q.dtype, q.n);
       if (o.p != q.p || o.ld != q.ld) apart("q", o, q);  // out may be q itself
+      off_cache("out", o, c);
     }
     const int64_t need = dreamer_attn_kv4_workspace(&c.c, (int)q.h);
     if (need) ws = at.memory({need}, at::kByte);  // returned to the stream's pool at the end

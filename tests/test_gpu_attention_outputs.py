@@ -23,3 +23,35 @@ def test_load_takes_both_outputs_or_none(cuda):
     assert (o == 5).all()
     k, v = c.load(cu, start, 6, out=(None, None))
     assert torch.equal(k, v) and (k != 0).any()
+
+
+def test_memory_of_the_cache_is_no_output(cuda):
+    """Nor what is stored: rows inside the cache's tensor, at its ends, of another depth."""
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    buf = torch.zeros(16384 + 2 * 4 * 4608 + 16384, dtype=torch.uint8, device="cuda")
+    c = KV4Cache(buf[16384:-16384].view(2, 2, 2, 1, 4608), 64)
+    cu, start, lens = _ints([0, 1, 2]), _ints([0, 0]), _ints([1, 1])
+    ok = torch.ones((2, 2, 64), device="cuda").bfloat16()
+
+    def at(byte):
+        return buf[byte:byte + 512].view(torch.bfloat16).view(2, 2, 64)
+
+    size = 2 * 4 * 4608
+    for byte in (16384 - 496, 16384, 16384 + size // 2, 16384 + size - 16):
+        x = at(byte)
+        for fn, args, kw in ((c.store, (x, ok, cu, start), {}), (c.store, (ok, x, cu, start), {}),
+                             (c.load, (cu, start, 2), dict(out=(x, ok))), (c.load, (cu, start, 2), dict(out=(ok, x))),
+                             (c.attend, (ok, lens), dict(out=x))):
+            with pytest.raises(ValueError):
+                fn(*args, **kw)
+    assert not buf.any()
+    for byte in (16384 - 512, 16384 + size):                    # right before it and behind it
+        x = at(byte)
+        x.copy_(torch.randn((2, 2, 64), device="cuda"))
+        c.store(x, x, cu, start)
+        k, _ = c.load(cu, start, 2, out=(x, ok))
+        assert k is x and c.attend(ok, lens, out=x) is x
+        # one key: its value is the output
+        want = c.load(cu, start, 2)[1]
+        assert torch.equal(x, want)
