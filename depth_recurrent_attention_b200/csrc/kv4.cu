@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
 // What bounds it is turning nibbles into operands (the integer pipe), so
 //   - bfloat16 runs on 8-bit integer products (m16n8k32): one mask makes four codes a word (the high
 //     halves of bytes enter as 16 c).
-//     q enters as a 16-bit fixed-point number of its plane's largest |q|, in two signed bytes, a weight
+//     q enters as a 16-bit fixed-point number of its plane's largest |q|, in two signed bytes (three where
+//     two would move a score by more than 2^-10: a channel far above the others, large queries), a weight
 //     p s as one of its column's largest in the block, in two unsigned bytes; the integer sums are
 //     exact.  The steps are 2^-15 and 2^-16 of the largest (half a step of bf16 is 2^-8 of the value
 //     itself, so q keeps its bf16 precision down to 1/128 of its plane's largest);
@@ -445,6 +446,32 @@ struct WarpAttn {
   float ofs[NG][2];    // sum of p m (of p (m + 8 s) where codes enter as c - 8)
   float m2[2], l2[2];
   uint32_t sel[NTI];   // 1 for the tile of column g, else 0
+  // INT: are two bytes of q enough?  A rounded q is off by 0.29 steps, a code is
+  // 8.7 (root mean squares), so a score of 64 channels is off by 20 s qi in log2; past 2^-10 (a weight off by
+  // 6.8e-4; a bf16 output is by 1.7e-3 alone) the queries get a third byte.  64 sequences of 4096, 16 heads of
+  // 64: 55 us with two bytes, 75 with three in every block (16 times larger queries).
+  float q_max;         // largest |qi| of this lane's columns
+  const T *qp;         // this lane's channels of column g's query head
+  bool live;           // a column with a query head (else zeros)
+
+  __device__ __forceinline__ void q_values(int p, float *v) const {
+    load8(qp + p * 64, v);
+    load8(qp + p * 64 + 8, v + 8);
+#pragma unroll
+    for (int e = 0; e < 16; e++)
+      if (!live) v[e] = 0.f;
+  }
+  // What 127 * 256 steps of a query's plane are: its largest |q|, or 2^-110 (the step stays a normal number).
+  // A q that is not finite leaves sum(q) so, and its scores with it.
+  __device__ __forceinline__ float q_top(const float *v, bool &ok) const {
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e++) amax = fmaxf(amax, fabsf(v[e]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    ok = amax <= 0x1.fffffep127f;
+    return ok ? fmaxf(amax, 0x1p-110f) : 1.f;
+  }
 
   // q as B fragments: column g is query head g % GP; a lane holds channels 16 t .. 16 t + 15 of a plane
   __device__ __forceinline__ void start(const T *q, int nq, float scale_log2) {
@@ -452,39 +479,32 @@ struct WarpAttn {
     const int qh = g % GP;
 #pragma unroll
     for (int ti = 0; ti < NTI; ti++) sel[ti] = g / GP == ti ? 1u : 0u;
-    const T *qp = q + (long)(qh < nq ? qh : 0) * D + 16 * t;
+    live = qh < nq;
+    qp = q + (long)(live ? qh : 0) * D + 16 * t;
 #pragma unroll
     for (int p = 0; p < NG; p++) {
       float v[16];
-      load8(qp + p * 64, v);
-      load8(qp + p * 64 + 8, v + 8);
-      float sum = 0.f, amax = 0.f;
+      q_values(p, v);
+      float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; e++) {
-        if (qh >= nq) v[e] = 0.f;
-        sum += v[e];
-        amax = fmaxf(amax, fabsf(v[e]));
-      }
+      for (int e = 0; e < 16; e++) sum += v[e];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int c0 = ((2 * t) % GP) * 4, c1 = ((2 * t + 1) % GP) * 4;
       qs[p][0] = __shfl_sync(0xffffffffu, sum, c0) * scale_log2;
       qs[p][1] = __shfl_sync(0xffffffffu, sum, c1) * scale_log2;
       if constexpr (INT) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 127 * 256 steps to the largest |q|, or to 2^-110 (the step stays a normal number); a q that is
-        // not finite leaves sum(q) so, and its scores with it
-        const bool ok = amax <= 0x1.fffffep127f;
-        const float top = ok ? fmaxf(amax, 0x1p-110f) : 1.f, step = top / 32512.f, inv = 32512.f / top;
+        bool ok;
+        const float top = q_top(v, ok), step = top / 32512.f, inv = 32512.f / top;
         qi[p][0] = __shfl_sync(0xffffffffu, step, c0) * scale_log2;
         qi[p][1] = __shfl_sync(0xffffffffu, step, c1) * scale_log2;
+        q_max = max3f(p == 0 ? 0.f : q_max, fabsf(qi[p][0]), fabsf(qi[p][1]));
 #pragma unroll
         for (int w = 0; w < 4; w++) {  // even channels of the low 8, odd ones, then of the high 8
           uint32_t hi = 0, lo = 0;
 #pragma unroll
           for (int e = 0; e < 4; e++) {
-            const int x = ok ? __float2int_rn(v[(w >> 1) * 8 + 2 * e + (w & 1)] * inv) : 0;
+            const int x = ok ? __float_as_int(fmaf(v[(w >> 1) * 8 + 2 * e + (w & 1)], inv, MAGIC_F)) - MAGIC : 0;
             const int h = (x + 128) >> 8;
             hi |= (uint32_t)(h & 255) << (8 * e);
             lo |= (uint32_t)((x - h * 256) & 255) << (8 * e);
@@ -582,6 +602,54 @@ struct WarpAttn {
     }
   }
 
+  // What rounding q to 16 bits left out of a block's scores: a third byte of every query
+  __device__ __forceinline__ void scores_rest(const uint8_t *blk, int my_key, float (*x)[4]) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+    for (int p = 0; p < NG; p++) {
+      float v[16];
+      q_values(p, v);
+      bool ok;
+      const float inv = 32512.f / q_top(v, ok);
+      uint32_t b[4];
+#pragma unroll
+      for (int w = 0; w < 4; w++) {  // in the order of start(), in steps of 1/254 of its own: half of one is 127
+        uint32_t r[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float u = v[(w >> 1) * 8 + 2 * e + (w & 1)], n = fmaf(u, inv, MAGIC_F) - MAGIC_F;
+          r[e] = __float_as_uint(fmaf(fmaf(u, inv, -n), 254.f, MAGIC_F));
+        }
+        b[w] = ok ? __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410) : 0u;
+      }
+      const float i0 = (p == 0 ? qi[0][0] : qi[NG - 1][0]) * (1.f / 254.f);
+      const float i1 = (p == 0 ? qi[0][1] : qi[NG - 1][1]) * (1.f / 254.f);
+#pragma unroll
+      for (int sp = 0; sp < NSUP; sp++) {
+        const uint8_t *kr = blk + p * PLANE + (sp * NTI * 16 + perm_row(g)) * 32 + 8 * t;
+        const int start[4] = {MAGIC, MAGIC, MAGIC, MAGIC};
+        int he[4], ho[4];
+#pragma unroll
+        for (int ti = 0; ti < NTI; ti++) {
+          const uint2 w0 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32);
+          const uint2 w1 = *reinterpret_cast<const uint2 *>(kr + ti * 16 * 32 + 8 * 32);
+          const uint32_t ev[4] = {w0.x & 0x0f0f0f0fu, w1.x & 0x0f0f0f0fu, w0.y & 0x0f0f0f0fu, w1.y & 0x0f0f0f0fu};
+          const uint32_t od[4] = {w0.x & 0xf0f0f0f0u, w1.x & 0xf0f0f0f0u, w0.y & 0xf0f0f0f0u, w1.y & 0xf0f0f0f0u};
+          mma16832<true>(he, ev, in_tile(b[0], ti), in_tile(b[2], ti), ti == 0 ? start : he);
+          mma16832<true>(ho, od, in_tile(b[1], ti), in_tile(b[3], ti), ti == 0 ? start : ho);
+        }
+        const uint8_t *kp = blk + 2 * NG * PLANE + p * PAIRS + (sp * NTI * 16 + my_key) * 4;
+        const float s0 = pair_at(kp).x, s1 = pair_at(kp + 8 * 4).x;
+        const float y[4] = {s0 * i0, s0 * i1, s1 * i0, s1 * i1};
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          const float f = fmaf(0.0625f, __int_as_float(ho[c]) - MAGIC_F, __int_as_float(he[c]) - MAGIC_F);
+          x[sp][c] = fmaf(y[c], f, x[sp][c]);
+        }
+      }
+    }
+  }
+
   // One block in shared memory: keys key0 .. key0 + 63, of which those below nkeys exist
   __device__ __forceinline__ void block(uint8_t *blk, int key0, int nkeys) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -595,7 +663,7 @@ struct WarpAttn {
       tc::fence_proxy_async();  // the next copy into this stage comes after these writes
       __syncwarp();
     }
-    float x[NSUP][4];
+    float x[NSUP][4], smax = 0.f;
 #pragma unroll
     for (int sp = 0; sp < NSUP; sp++) {
 #pragma unroll
@@ -604,6 +672,7 @@ struct WarpAttn {
         products(blk, sp, p, f);
         const uint8_t *kp = blk + 2 * NG * PLANE + p * PAIRS + (sp * NTI * 16 + my_key) * 4;
         const float2 s0 = pair_at(kp), s1 = pair_at(kp + 8 * 4);
+        if constexpr (INT) smax = max3f(smax, s0.x, s1.x);
         const float z0 = INT ? s0.y : fmaf(8.f, s0.x, s0.y), z1 = INT ? s1.y : fmaf(8.f, s1.x, s1.y);
         const float y0 = fmaf(s0.x * qi[p][0], f[0], z0 * qs[p][0]), y1 = fmaf(s0.x * qi[p][1], f[1], z0 * qs[p][1]);
         const float y2 = fmaf(s1.x * qi[p][0], f[2], z1 * qs[p][0]), y3 = fmaf(s1.x * qi[p][1], f[3], z1 * qs[p][1]);
@@ -613,6 +682,8 @@ struct WarpAttn {
         x[sp][3] = p == 0 ? y3 : x[sp][3] + y3;
       }
     }
+    if constexpr (INT)
+      if (__any_sync(0xffffffffu, smax * q_max > 0x1p-10f / 20.f)) scores_rest(blk, my_key, x);
     if (tail) {
 #pragma unroll
       for (int sp = 0; sp < NSUP; sp++) {
@@ -914,8 +985,8 @@ __device__ __forceinline__ void cluster_sync() {
 // Cluster form (one launch): a cluster of CTAs takes one (sequence, key head, chunk of GP
 // query heads), every CTA a contiguous share of its blocks, every warp each NW-th block of that;
 // warps join in shared memory, CTAs in distributed shared memory.
-template <typename T, int NG, int GP, int NW, int ST>
-__global__ void __launch_bounds__(NW * 32) kv4_attn_kernel(AttnArgs a) {
+template <typename T, int NG, int GP, int NW, int ST, int OCC>
+__global__ void __launch_bounds__(NW * 32, OCC) kv4_attn_kernel(AttnArgs a) {
   using W = WarpAttn<T, NG, GP>;
   constexpr int D = W::D, BLK = W::BLK;
   extern __shared__ __align__(128) uint8_t ring_mem[];  // rings; then [NW][GP][D] partial outputs
@@ -1432,7 +1503,7 @@ int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
                                                        share);
   }
   constexpr int part = C::NW * GP * W::D * 4, rings = C::NW * C::ST * W::BLK;
-  return launch<kv4_attn_kernel<T, NG, GP, C::NW, C::ST>>(dim3((unsigned)(items * p.cluster)), dim3(C::NW * 32),
+  return launch<kv4_attn_kernel<T, NG, GP, C::NW, C::ST, C::OCC>>(dim3((unsigned)(items * p.cluster)), dim3(C::NW * 32),
                                                           rings > part ? rings : part, p.cluster, s, o, a);
 }
 

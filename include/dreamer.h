@@ -282,8 +282,11 @@ int dreamer_kv4_load(const dreamer_kv4_cache *cache, void *k, int64_t ldk, void 
  *   out = sum_i softmax_i(scale q . k_i) v_i,
  * and a sequence with lens[b] = 0 gets zeros.  q, out: [batch] rows of n_heads * head_dim of
  * dtype (out may be q); lens [batch] int32; n_heads a multiple of n_kv_heads.  Sums and softmax
- * are float32; bfloat16 takes q, and a 64-token block's weights, as 16-bit fixed-point numbers of
- * their largest (of 64 channels; of the block), float32 works to float32 precision throughout.
+ * are float32; bfloat16 takes q, and a 64-token block's weights times their values' s, as 16-bit
+ * fixed-point numbers of their largest (of 64 channels; of the block), q in 24 bits where 16 would
+ * move a score by 2^-10 (in log2, root mean square); weights stay at 16, so a token whose value
+ * scale s is R times those of its block adds an error of about R 5e-6 to theirs.  float32 works to
+ * float32 precision throughout.
  * What lies in the cache behind lens[b] is not used.
  * After an expired wait (status) the outputs that wanted the missing keys are NaN.
  * workspace: device memory of at least dreamer_attn_kv4_workspace() bytes (NULL where that is 0),
