@@ -13,7 +13,8 @@
 // What a row must not see does not touch it, whatever it holds: masked scores are replaced, not
 // added to; value rows behind the prompt's end are cleared in shared memory; and where a value
 // of the diagonal block is not finite (0 x infinity would reach the rows before it), the block's
-// output product is done row by row on CUDA cores up to the row's own position.
+// output product is done row by row on CUDA cores up to the row's own position. (The order of its
+// float32 sums is another there: the tile's rows may store a neighbouring bfloat16.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
