@@ -72,7 +72,8 @@ __device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu,
   __syncthreads();
   if (tid < ROWS) {
     const int r = row0 + tid;
-    int p = -1, b = -1, off = 0;
+    int p = -1, b = -1;
+    long off = 0;
     if (r < a.n_rows) {
       if (!a.cu) {
         b = r;
@@ -85,11 +86,11 @@ __device__ __forceinline__ void find_slots(const RowArgs &a, int row0, int *scu,
         }
         if (lo < a.B && cu[lo] <= r) {
           b = lo;
-          off = r - cu[lo];
+          off = (long)r - cu[lo];
         }
       }
       if (b >= 0) {
-        const long q = (long)a.start[b] + off;
+        const long q = a.start[b] + off;
         if (q >= 0 && q < a.limit) p = (int)q;
         else raise_dev_error(a.err, DEV_BAD_INDEX);
       }

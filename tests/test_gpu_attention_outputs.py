@@ -55,3 +55,20 @@ def test_memory_of_the_cache_is_no_output(cuda):
         # one key: its value is the output
         want = c.load(cu, start, 2)[1]
         assert torch.equal(x, want)
+
+
+def test_boundaries_and_starts_at_the_ends_of_32_bits(cuda):
+    """A first boundary far below 0 (rows behind it belong to the sequence) and a start near 2^31: the position
+    is their sum, outside the cache, and nothing wraps around into it."""
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    c = KV4Cache.alloc(1, 2, 64, 64)
+    x = torch.randn((4, 2, 64), device="cuda").bfloat16()
+    for first, start in ((-2 ** 31, 2 ** 31 - 1), (-2 ** 31, 2 ** 31 - 4), (-2 ** 31, -5), (-9, 2 ** 31 - 1)):
+        st = _ints([0])
+        c.store(x, x, _ints([first, 4]), _ints([start]), status=st)
+        assert st.item() != 0 and not c.data.any(), (first, start)
+    st = _ints([0])
+    c.store(x, x, _ints([-9, 4]), _ints([3]), status=st)       # row 0 is the sequence's tenth
+    k, _ = c.load(_ints([0, 4]), _ints([12]), 4)
+    assert st.item() == 0 and (k != 0).any(-1).all()
