@@ -102,7 +102,7 @@ float scale_of(PyObject *o, int64_t d) {
   if (o == Py_None) return (float)(1.0 / sqrt((double)d));
   const double s = PyFloat_AsDouble(o);
   if (s == -1.0 && PyErr_Occurred()) throw Refused();
-  if (!isfinite((float)s)) refuse("scale: a finite number");
+  if (!isfinite((float)s * 1.4426950408889634f)) refuse("scale: a number below 2.3e38");  // as the library
   return (float)s;
 }
 

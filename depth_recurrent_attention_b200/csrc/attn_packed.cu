@@ -916,7 +916,7 @@ int attn_packed(const PackedAttn &p, cudaStream_t s, LaunchOpt o) {
   a.cu = p.cu; a.n_seq = p.n_seq; a.n_tokens = p.n_tokens; a.Hq = p.Hq; a.G = p.Hq / p.Hkv;
   a.q = p.q; a.k = p.k; a.v = p.v; a.ldq = p.ldq; a.ldk = p.ldk; a.ldv = p.ldv;
   a.out = p.out; a.ldo = p.ldo; a.out_rows = p.out_rows;
-  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.scale_log2 = p.scale * LOG2_E;
   a.err = p.err;
 #ifdef DREAMER_TEST_HOOKS
   a.withhold = take_withhold();
@@ -950,7 +950,7 @@ extern "C" int dreamer_attn_packed(const void *q, int64_t ldq, const void *k, in
                                    float scale, int32_t *status, dreamer_stream stream) {
   if (!q || !k || !v || !out || !cu_seqlens || n_seq < 0 || n_tokens < 0) return DREAMER_ERR_ARG;
   if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || head_dim < 1) return DREAMER_ERR_ARG;
-  if ((dtype != 0 && dtype != 1) || !(scale > 0.f) || !isfinite(scale)) return DREAMER_ERR_ARG;
+  if ((dtype != 0 && dtype != 1) || !(scale > 0.f) || !ops::scale_ok(scale)) return DREAMER_ERR_ARG;
   if (head_dim != 64 && head_dim != 128 && (dtype == 1 || (head_dim != 16 && head_dim != 32)))
     return DREAMER_ERR_UNSUPPORTED;
   const int es = dtype == 0 ? 4 : 2;

@@ -1554,7 +1554,7 @@ int kv4_attn(const Kv4Cache &c, const Kv4Attn &t, cudaStream_t s, LaunchOpt o) {
   a.q = t.q; a.ldq = t.ldq; a.out = t.out; a.ldo = t.ldo;
   a.lens = t.lens; a.len_add = t.len_add;
   a.limit = t.limit ? t.limit : c.cap;
-  a.scale_log2 = t.scale * 1.4426950408889634f;
+  a.scale_log2 = t.scale * LOG2_E;
   a.err = t.err;
   a.part = (float *)t.workspace;
 #ifdef DREAMER_TEST_HOOKS
@@ -1653,7 +1653,7 @@ extern "C" int dreamer_attn_kv4(const dreamer_kv4_cache *c, const void *q, int64
   const int rc = check_cache(c);
   if (rc) return rc;
   if (!q || !out || !lens || n_heads < 1 || n_heads % c->n_kv_heads || (dtype != 0 && dtype != 1) ||
-      !isfinite(scale))
+      !ops::scale_ok(scale))
     return DREAMER_ERR_ARG;
   const int es = dtype == 0 ? 4 : 2;
   const int64_t w = (int64_t)n_heads * c->head_dim;

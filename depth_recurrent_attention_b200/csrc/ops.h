@@ -3,6 +3,7 @@
 // DREAMER_* code for what only it can see (a tensor map, a CUDA error).
 #pragma once
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -41,6 +42,10 @@ inline LaunchOpt user_launch(cudaStream_t s) {
   else cudaGetLastError();
   return o;
 }
+
+// softmax in powers of two; a scale that this takes out of float32 is refused
+constexpr float LOG2_E = 1.4426950408889634f;
+inline bool scale_ok(float scale) { return isfinite(scale * LOG2_E); }
 
 // Launch of one kernel (a template argument, so that what is noted of it is its own).  Its limit of
 // dynamic shared memory is raised once a device, noted in bit d of `raised`, and again where a launch

@@ -225,7 +225,7 @@ int dreamer_route_balance(dreamer_handle *h, int depth, float *lorenz, float *gi
  *   out[t] = sum_{i <= t} softmax_i(scale q[t] . k[i]) v[i].
  * q, out: n_tokens rows of n_heads * head_dim, k, v: of n_kv_heads * head_dim, of dtype (0 =
  * float32, 1 = bfloat16), at strides ld* (elements, a multiple of 16 bytes), 16-byte aligned.
- * out must not overlap q, k or v.  scale > 0.  Rows of no prompt are neither used nor written.
+ * out must not overlap q, k or v.  0 < scale < 2.3e38.  Rows of no prompt are neither used nor written.
  * bfloat16: head_dim 64 or 128, tensor cores with float32 sums and softmax, weights of the
  * output product rounded to bfloat16.  float32: head_dim 16, 32, 64 or 128, CUDA cores.
  * `status` is NULL or a device int32 that the caller clears: set non-zero by boundaries that are
@@ -279,7 +279,7 @@ int dreamer_kv4_load(const dreamer_kv4_cache *cache, void *k, int64_t ldk, void 
 
 /* Attention of one query token a sequence over the cache, grouped heads: query head j of
  * sequence b attends positions 0 .. lens[b]-1 of key head j / (n_heads / n_kv_heads),
- *   out = sum_i softmax_i(scale q . k_i) v_i,
+ *   out = sum_i softmax_i(scale q . k_i) v_i,   |scale| < 2.3e38,
  * and a sequence with lens[b] = 0 gets zeros.  q, out: [batch] rows of n_heads * head_dim of
  * dtype (out may be q); lens [batch] int32; n_heads a multiple of n_kv_heads.  Sums and softmax
  * are float32; bfloat16 takes q, and a 64-token block's weights times their values' s, as 16-bit
