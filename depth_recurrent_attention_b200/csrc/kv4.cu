@@ -1439,18 +1439,18 @@ RowArgs row_args(const Kv4Cache &c, const Kv4Rows &r) {
 dim3 row_grid(const RowArgs &a, int rows) {
   return dim3((a.n_rows + rows - 1) / rows, (a.Hkv * a.ng + 7) / 8, 2);
 }
-// 64 rows a CTA from two CTAs an SM on
-bool many_rows(const RowArgs &a) {
-  const dim3 g = row_grid(a, 64);
-  return (long)g.x * g.y * g.z >= 2 * 148;
-}
-
 int device_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return 148;
   return sms;
+}
+
+// 64 rows a CTA from two CTAs an SM on
+bool many_rows(const RowArgs &a) {
+  const dim3 g = row_grid(a, 64);
+  return (long)g.x * g.y * g.z >= 2L * device_sms();
 }
 
 // Warps a CTA, ring stages and CTAs an SM (a third stage, or a fifth CTA, measured no faster)
