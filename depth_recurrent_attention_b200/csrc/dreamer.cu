@@ -1017,6 +1017,7 @@ static void run_depth(dreamer_handle *h, int l, bool first, bool last, const Dep
       a4.lens = io.cache_len; a4.len_add = 1; a4.Hq = c.n_heads; a4.dtype = c.dtype;
       a4.scale = 1.0f / sqrtf((float)d); a4.workspace = h->kv4_ws; a4.err = h->err; a4.limit = c.max_cache_len;
       ops::LaunchOpt o;
+      o.next = h->use_pdl && !h->prof;
       o.pdl = pdl_take(h, st);
       if (ops::kv4_store(c4, r4, st, o) != DREAMER_OK) h->path_err = 1;
       o.pdl = pdl_take(h, st);

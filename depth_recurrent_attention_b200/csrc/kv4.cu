@@ -1496,7 +1496,7 @@ int launch_attn(AttnArgs a, cudaStream_t s, LaunchOpt o) {
                                                                              C::NW * C::ST * W::BLK, 1, s, o, a);
     if (rc) return rc;
     LaunchOpt j;
-    j.pdl = true;  // the split kernel precedes it on the stream
+    j.pdl = o.next;  // the split kernel precedes it on the stream
     // warps a query head: one for each four of the slots that items have on average
     const long outs = (long)a.B * a.Hkv * a.G, mean = a.n_warps / items;
     const int share = mean > 64 ? 8 : mean > 32 ? 4 : mean > 8 ? 2 : 1;

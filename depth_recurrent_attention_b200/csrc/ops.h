@@ -31,7 +31,8 @@ inline Withhold take_withhold() {
 // Launch options: programmatic dependent launch (the kernel waits by itself for what ran before on
 // the stream, so its blocks may be placed meanwhile).
 struct LaunchOpt {
-  bool pdl = false;
+  bool pdl = false;   // the call's first kernel
+  bool next = true;   // its further ones, which follow a kernel of the call
 };
 // of a call on a user's stream: programmatic unless the stream is being captured, where the edge from
 // an operation that is no kernel could not be

@@ -46,3 +46,31 @@ def test_a_refused_decode_position_changes_nothing_in_the_cache(cuda, dtype, cap
         same = torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
         assert same, bad
     dev.close()
+
+
+def test_decode_without_programmatic_launches(cuda, monkeypatch):
+    """DREAMER_NO_PDL and stage profiling launch every kernel after the one before has ended: the same bits."""
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    from depth_recurrent_attention_b200.dreamer import Dreamer
+    cfg = configs.SMALL.with_(batch=2, seq=64, depth=2, cache_len=0, n_experts=4, top_k=4)
+    W = {k: inputs.to_device(v, "fp32" if k == "bias" else cfg.dtype) for k, v in inputs.host_weights(cfg).items()}
+    x = inputs.to_device(inputs.extra_normal(cfg, 7300, (2, cfg.hidden), 1.0), cfg.dtype)
+    lens = _ints([12000, 70])                                   # the split form and its join
+    data = torch.randint(0, 60, (2, 2, 8, 13056 // 64, 4608), dtype=torch.uint8, device="cuda")
+
+    def step(profile=False):
+        dev = Dreamer(cfg, W, max_cache_len=13000)
+        if profile:
+            dev.set_profiling(True)
+        c = KV4Cache(data.clone(), 64)
+        out = [dev.decode_step_kv4(x, c, lens).clone() for _ in range(3)]
+        dev.route_counts()
+        dev.close()
+        return out
+
+    want = step()
+    got = step(profile=True)
+    monkeypatch.setenv("DREAMER_NO_PDL", "1")
+    for a, b, c in zip(want, got, step()):
+        assert torch.equal(a, b) and torch.equal(a, c)
