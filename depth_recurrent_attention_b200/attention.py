@@ -67,8 +67,9 @@ def attn_packed(q, k, v, cu_seqlens, out=None, scale=None, status=None, stream=N
     not decreasing: prompt i holds rows cu_seqlens[i] .. cu_seqlens[i+1]-1.  Query head j uses key
     head j // (n_heads // n_kv_heads); scale (positive) defaults to 1 / sqrt(dim).  Returns
     `out`, [tokens][n_heads][dim], which must not overlap q, k or v (it may be other columns of their
-    buffer); rows of no prompt are not written.  bfloat16 takes dim 64 and
-    128, float32 also 16 and 32.  Boundaries out of order or outside the rows set `status`."""
+    buffer).  Rows of no prompt are not written: they keep what `out` held, and without a given `out`
+    what its new memory held.  bfloat16 takes dim 64 and 128, float32 also 16 and 32.  Boundaries out of
+    order or outside the rows set `status`; rows that then lie in several prompts are undefined."""
     return _done(_ext.attn_packed(q, k, v, cu_seqlens, out, scale, status, stream), "dreamer_attn_packed")
 
 

@@ -47,7 +47,8 @@ struct PackedArgs {
 #endif
 };
 
-// First row and length of prompt i; boundaries outside 0 .. n_tokens or decreasing are cut.
+// First row and length of prompt i; boundaries outside 0 .. n_tokens are cut, and an end before its start.
+// Boundaries that decrease (reported) can leave rows in two prompts, whose blocks then both write them.
 __device__ __forceinline__ int2 prompt_rows(const PackedArgs &a, int i) {
   const int lo = min(max(a.cu[i], 0), a.n_tokens);
   const int hi = min(max(a.cu[i + 1], lo), a.n_tokens);

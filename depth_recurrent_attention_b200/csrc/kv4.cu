@@ -187,9 +187,9 @@ __device__ __noinline__ float step_exact(float mx, float mn) { return (float)(((
 
 // Eight codes of a lane's values, four bits each.  The quotient in 32 bits is off by less than 2^-18,
 // so it rounds as the exact one does unless that lies within 2^-16 of a half, which the remainder
-// d - c s (exact: at most 20 bits) shows.  There the remainder decides where d = x - m is
+// d - c s (exact: at most 24 bits) shows.  There the remainder decides where d = x - m is
 // exact, as it nearly always is for bfloat16 (a tie goes to the even code), else the form in 64 bits.
-// bfloat16: m is the minimum itself and s within 2^-9 of a 15th, so quotients lie in 0 .. 15.1.
+// bfloat16: m is the minimum itself and s within 2^-8 of a 15th, so quotients lie in 0 .. 15.06.
 template <typename T>
 __device__ __forceinline__ uint32_t codes8(const Raw8<T> &x, float m, float s) {
   constexpr bool CLAMP = sizeof(T) == 4;
