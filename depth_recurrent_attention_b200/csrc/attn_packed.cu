@@ -132,8 +132,8 @@ __device__ __forceinline__ void check_cu(const PackedArgs &a) {
 // An SM holds two 128-query tiles: at head dim 128 one CTA takes two adjacent tiles A, B of a prompt and
 // a head that share every K/V block; at 64 there are two CTAs of one tile (A) each, and while one starts
 // or ends its item the other computes (8 ragged prompts of up to 2048 tokens, 16 heads: 66.4 -> 63.2 us;
-// one prompt of 8192: 244 -> 242).  Warp 0 loads Q and K by TMA, warp 2 V, warp 1 issues the MMAs, warps
-// 4 and up hold one query row a thread.
+// one prompt of 8192: 244 -> 242 under the power cap, 215 at 1965 MHz).  Warp 0 loads Q and K by TMA, warp
+// 2 V, warp 1 issues the MMAs, warps 4 and up hold one query row a thread.
 // Scores, weights and outputs stay in tensor memory; the output is rescaled only when a row's maximum
 // grows by more than 2^8.  Weights enter the output product as bf16 (half a step of 2^-8 relative each, as
 // the stored output is), their sum is of the float32 values.
@@ -147,7 +147,8 @@ __device__ __forceinline__ void check_cu(const PackedArgs &a) {
 // So
 //   - head dim 64 keeps the weights in tensor-memory columns of their own, and the next block's
 //     scores are computed as soon as this block's are in registers (one sequence of 8192 tokens, 16
-//     heads of 64: 248 -> 231 us); at 128 tensor memory is full, the weights lie over their scores;
+//     heads of 64, two tiles a CTA: 248 -> 231 us at one clock); at 128 tensor memory is full, the weights
+//     lie over their scores;
 //   - the products are issued by a converged warp's elected lane (3 to 6 % against one lane of a split
 //     warp).
 // A polynomial for a part of the exponentials (2 to 5 of every 8 pairs) cost 1 to 14 %, the weights handed

@@ -363,8 +363,9 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(RowArgs a) {
 // The rows r of a 16-key tile are the keys perm_row(r): with it a warp's 8-byte reads of K rows and
 // 4-byte reads of V rows meet every bank once.
 //
-// Measured: the decode workload's depth (64 sequences of 4096 tokens, 16 heads of 64, 302 MB) 53 us, 5.7
-// TB/s, with the cluster form at one CTA an item; products on bf16 numbers instead of bytes took 82.
+// Measured: the decode workload's depth (64 sequences of 4096 tokens, 16 heads of 64, 302 MB) 53 us replayed
+// from a graph (5.7 TB/s), 60 a call among others (5.0), with the cluster form at one CTA an item; products
+// on bf16 numbers instead of bytes took 82.  float32 (three terms): 122.
 struct AttnArgs {
   const uint8_t *data;
   int B, Hkv, cap, Hq, G, qchunks;
@@ -1464,10 +1465,14 @@ int heads_a_chunk(int G) { return G <= 2 ? 2 : G <= 4 ? 4 : 8; }
 
 // How the items are spread over the GPU's `slots` CTAs, from the number of items and the most blocks
 // of one (the lengths are known on the device only).  A cluster form's CTAs join by themselves, the
-// hardware hands out what does not fit at once, and equal lengths keep every warp busy: 1024 items of
-// 4096 tokens, head dim 64, 52 us against 59 of the split form.  The split form pays a second launch and
-// evens out what a single wave cannot: items fewer than slots with long runs of blocks a warp (4
-// items of 131071 tokens, head dim 128, 86 -> 27 us; 128 of 1 to 8192 tokens 31 -> 21, all of 8192 37 -> 38).
+// hardware hands out what does not fit at once, and equal lengths keep every warp busy.  The split form
+// pays a second launch and evens out what a single wave cannot.  Its time against the cluster form's, both
+// forced, bfloat16, 4 to 512 items of one head of 64 and of four of 128, all of the full length | ragged:
+//   clusters of 8:      4 blocks a warp -2 .. +25 % | -3 .. +15;   6: -18 .. +17 | -17 .. +8;   16: -41 .. +8 | -42 .. -14
+//   of 4, 2, no others: 8 blocks a warp +15 .. +23 % | -8 .. +15;  12: +9 .. +16 | -28 .. +10;  16: +7 .. +13 | -26 .. -2;
+//                       32 to 128: -9 .. -1 | -54 .. -14
+// so from 6 and 12 blocks on the split form is taken, for lengths that differ: 128 items of up to 12288 tokens 45 ->
+// 24 us, all of 12288 51 -> 50; 4 of 32768 26 -> 15.
 struct Plan {
   int cluster;
   bool split;
