@@ -730,6 +730,9 @@ static void launch_rows(dreamer_handle *h, const RowsArgs &a, int d, cudaStream_
 // other SMs, from per-SM rates measured on B200: DA about DA_BYTES_SM bytes/s an SM, up to
 // DA_BYTES_ALL over the whole chip; flash SA about SA_FLOPS_SM_D128 (head dim 128) or
 // SA_FLOPS_SM_D64 flop/s an SM.  0 when the split does not pay (DA then runs at full width).
+// Packed prompts are planned as equal ones of their mean length, at the same rates; their kernel is
+// faster (3.8e12 and 6.5e12 alone) and ragged ones cost more than that, so SA may end first or last there.
+// 8 prompts of 2048, medium workload: 14.9 ms packed, 15.1 as an equal-length forward.
 static constexpr double DA_BYTES_SM = 26e9, DA_BYTES_ALL = 4.7e12;
 static constexpr double SA_FLOPS_SM_D128 = 5.3e12, SA_FLOPS_SM_D64 = 2.5e12;
 static int da_beside_sa_sms(const dreamer_handle *h, int l, int r0, double n_prompts, double len) {
