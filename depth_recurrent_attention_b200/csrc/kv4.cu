@@ -657,11 +657,11 @@ struct WarpAttn {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int my_key = ((2 * t) / GP) * 16 + perm_row(g);  // in a supertile: this lane's keys my_key (+ 8)
     const bool tail = key0 + KV4_BLOCK > nkeys;
-    if (tail) {  // what lies behind the last key may be anything: its values count as zero
+    if (tail) {  // what lies behind the last key may be anything: its keys and values count as zero
       for (int k = lane; k < KV4_BLOCK; k += 32)
         if (key0 + k >= nkeys)
 #pragma unroll
-          for (int p = 0; p < NG; p++) *reinterpret_cast<uint32_t *>(blk + 2 * NG * PLANE + (NG + p) * PAIRS + k * 4) = 0;
+          for (int p = 0; p < 2 * NG; p++) *reinterpret_cast<uint32_t *>(blk + 2 * NG * PLANE + p * PAIRS + k * 4) = 0;
       tc::fence_proxy_async();  // the next copy into this stage comes after these writes
       __syncwarp();
     }

@@ -84,3 +84,26 @@ def test_queries_of_any_spread(cuda, kind, lens, H, G, d, capacity):
     tol = np.sqrt((2.0 ** -16 / 3) * (want ** 2).sum() + (3 * E) ** 2 * (spread ** 2).sum())
     err = np.sqrt(((got - want) ** 2).sum())
     assert err <= tol, (err / np.sqrt((want ** 2).sum()), tol / np.sqrt((want ** 2).sum()), moved * 20)
+
+
+@pytest.mark.parametrize("capacity", [192, 192 * 70])
+@pytest.mark.parametrize("pair", [0x7F7F, 0x7F80, 0x4700])      # a scale and offset of 3.4e38, infinity, 2^15
+def test_scales_behind_the_last_key_change_no_bit(cuda, pair, capacity):
+    """Whether a block's queries get their third byte is decided by the keys that count."""
+    import torch
+    from depth_recurrent_attention_b200.attention import KV4Cache
+    rng = np.random.default_rng(31)
+    lens, d = [70, 64, 1, 0], 128
+    c = KV4Cache.alloc(4, 2, d, capacity)
+    k, v = rng.standard_normal((2, 520, 2, d))
+    c.store(_bf16(k), _bf16(v), _ints(range(0, 521, 130)), _ints([0] * 4))
+    q = _bf16(rng.standard_normal((4, 4, d)))
+    a = c.attend(q, _ints(lens))
+    nb = capacity // 64
+    pos = torch.arange(capacity, device="cuda").view(nb, 64)
+    pairs = c.data[0].view(4, 2, nb, -1)[..., 4 * 64 * 32:].view(torch.int16).view(4, 2, nb, 4, 64, 2)
+    for b, n in enumerate(lens):
+        hidden = (pos >= n)[None, :, None, :, None].expand(2, nb, 4, 64, 2)
+        pairs[b][hidden] = pair
+    same = torch.equal(a, c.attend(q, _ints(lens)))
+    assert same
