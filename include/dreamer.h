@@ -230,8 +230,8 @@ int dreamer_route_balance(dreamer_handle *h, int depth, float *lorenz, float *gi
  * output product rounded to bfloat16.  float32: head_dim 16, 32, 64 or 128, CUDA cores.
  * `status` is NULL or a device int32 that the caller clears: set non-zero by boundaries that are
  * not as above or by an expired bounded wait (some rows are then not written).  Prompts of such
- * boundaries are cut at the rows' ends; where they overlap each other, a row in several holds the
- * output of any of them, of one call or of another.  Asynchronous on `stream`, on the current device. */
+ * boundaries are cut at the first and last row; a row that then lies in several holds the output of
+ * any one of them.  Asynchronous on `stream`, on the current device.                         */
 int dreamer_attn_packed(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
                         int64_t ldv, void *out, int64_t ldo, const int32_t *cu_seqlens, int n_seq,
                         int n_tokens, int n_heads, int n_kv_heads, int head_dim, int dtype,
